@@ -69,10 +69,13 @@ extern "C" {
 #define TQ_ERR_MISMATCH       -6  /* codebook does not match the call's d/b  */
 #define TQ_ERR_SCRATCH_LIMIT  -7  /* tq_topk_noalloc: sizes need more scratch
                                      than TQ_NOALLOC_SCRATCH_BYTES            */
+#define TQ_ERR_PAGES          -8  /* tq_kv8_reserve: not enough free pages (a
+                                     device status, see tq_device_status)     */
 
 /* element types of caller inputs */
 #define TQ_F32  0
 #define TQ_BF16 1
+#define TQ_F16  2  /* tq_rope and the tq_kv8_* calls only */
 
 /* operation ids for tq_workspace_bytes */
 #define TQ_OP_BUILD   0
@@ -192,7 +195,9 @@ TQ_API int tq_encode(const tq_codebook_t *cb, const float *d_Pi, const float *d_
  * (its first 4 bytes): TQ_OK, or TQ_ERR_DEVICE_TIMEOUT when a bounded
  * device-side wait of a tensor-core kernel gave up (the kernel then drains its
  * in-flight copies and MMAs, releases tensor memory and exits; its outputs are
- * undefined).  Copies the word to the host and synchronises `stream`. */
+ * undefined).  The page operations of the 8-bit cache record TQ_ERR_ARG or
+ * TQ_ERR_PAGES there, tq_kv8_attention a time-out.  Copies the word to the host
+ * and synchronises `stream`. */
 TQ_API int tq_device_status(const void *d_ws, void *stream);
 
 /* Self-test of the device-side time-out path (no counterpart on the pages):
@@ -339,6 +344,176 @@ TQ_API int tq_topk_noalloc(const tq_codebook_t *cb, const float *d_Pi, const flo
                            int G, int64_t n, const uint32_t *d_codes, const float *d_xnorm,
                            const float *d_rnorm, int nq, const void *d_q, int q_dtype, int k,
                            float *d_vals, int64_t *d_ids, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and a paged KV cache in 8 bits.
+ *
+ * The records above spend 1.5 to 4 bits on a coordinate.  This cache spends 8
+ * (signed integers or e4m3, one fp32 scale for each page of tokens and KV
+ * head), for models and layers that need the precision; many sequences of
+ * unlike length share its pages.  The pages of the reference have no
+ * counterpart: page pools, block scales and rotary positions are standard
+ * serving practice around the attention that its KV-cache paragraphs feed.
+ * ------------------------------------------------------------------------- */
+
+/* pairing of the rotated coordinates */
+#define TQ_ROPE_HALF        0  /* coordinate i with i + rot/2     */
+#define TQ_ROPE_INTERLEAVED 1  /* coordinate 2i with 2i + 1       */
+
+/* frequency rules */
+#define TQ_ROPE_PLAIN  0  /* f_i = base^(-2i/rot)                                     */
+#define TQ_ROPE_LINEAR 1  /* f_i / factor                                             */
+#define TQ_ROPE_NTK    2  /* base replaced by base * factor^(rot/(rot-2)); rot >= 4   */
+#define TQ_ROPE_PARTS  3  /* with r_i = ctx f_i / 2 pi (turns within the original
+                             context) and g_i = clamp((r_i - low)/(high - low), 0, 1):
+                             f_i (g_i + (1 - g_i)/factor)                             */
+
+/* Rotation parameters (host, plain data, filled by tq_build_rope, passed by
+ * value to the kernels).  turns[i] = f_i / 2 pi in turns, as a fraction of 2^64:
+ * position times turns[i], modulo 2^64, is the exact fraction of a turn, so an
+ * angle keeps its precision at every 64-bit position (no tables). */
+typedef struct tq_rope_params {
+    int32_t  d;          /* head dimension, even, 2..256                      */
+    int32_t  rot;        /* rotated coordinates (the first ones), even, 0..d  */
+    int32_t  layout;     /* TQ_ROPE_HALF or TQ_ROPE_INTERLEAVED               */
+    float    amplitude;  /* factor of the rotated coordinates (usually 1)     */
+    uint64_t turns[128];
+} tq_rope_params_t;
+
+/* Fills *r (host only, fp64).  scaling: a rule above; factor >= 1 (ignored by
+ * PLAIN); ctx, low, high: PARTS only (ctx > 0, low < high).  base > 1.
+ * TQ_ERR_ARG for a bad enum or a non-finite or out-of-range number,
+ * TQ_ERR_UNSUPPORTED for d or rot outside the ranges above. */
+TQ_API int tq_build_rope(int d, int rot, double base, int layout, int scaling, double factor,
+                         double ctx, double low, double high, double amplitude,
+                         tq_rope_params_t *r);
+
+/* Rotary positions: for token t, head h and every pair (x1, x2) with angle
+ * p f_i at position p = d_pos[t] (any int64),
+ *   y1 = a (x1 cos - x2 sin),  y2 = a (x2 cos + x1 sin),
+ * the coordinates behind `rot` copied.  transpose = 1 applies the transposed
+ * matrix (sin -> -sin): the gradient of x from that of y (and, with a = 1, the
+ * inverse rotation).  x: [T][heads][d] of x_dtype (TQ_F32, TQ_BF16 or TQ_F16)
+ * with strides of x_ts (token) and x_hs (head) elements, the coordinates of a
+ * head contiguous; out likewise (may be x itself with equal strides; no other
+ * overlap).  fp32 arithmetic, one rounding to x_dtype.  T = 0 is a no-op. */
+TQ_API int tq_rope(const tq_rope_params_t *r, int64_t T, int heads, const void *d_x,
+                   int64_t x_ts, int64_t x_hs, int x_dtype, const int64_t *d_pos, void *d_out,
+                   int64_t out_ts, int64_t out_hs, int transpose, void *stream);
+
+/* code formats of the cache */
+#define TQ_KV_I8   0  /* signed bytes -127..127, scale = max|x| / 127 */
+#define TQ_KV_E4M3 1  /* e4m3 (no infinities), scale = max|x| / 448   */
+
+/* A paged cache (host struct of device pointers; the caller owns everything).
+ * A slot is a sequence: a row of the table and a length in tokens; token j of a
+ * slot lies in page table[j / page] at row j % page.  A page belongs to all
+ * layers at once.  refs counts the slots that hold a page (0: free).  A key or
+ * value is scale * code; rows of a page that no token was written to may hold
+ * any bytes (none of the calls below reads them into a result).
+ * Limits: d 64 or 128; page 16, 32, 64 or 128; heads, layers, slots,
+ * max_pages, pages >= 1; pages * heads * page < 2^31; d_k and d_v 16-byte
+ * aligned. */
+typedef struct tq_kv8 {
+    int32_t d, heads, page, format;
+    int32_t layers, slots, max_pages, pages;
+    void    *d_k, *d_v;            /* [layers][pages][heads][page][d] bytes */
+    float   *d_kscale, *d_vscale;  /* [layers][pages][heads]                */
+    int32_t *d_table;              /* [slots][max_pages] page ids; -1: none */
+    int32_t *d_len;                /* [slots]                               */
+    int32_t *d_refs;               /* [pages]                               */
+} tq_kv8_t;
+
+/* operation ids for tq_kv8_workspace_bytes */
+#define TQ_KV8_OP_PAGES     0  /* reserve, fork, truncate, compact: n = list entries (compact: 0) */
+#define TQ_KV8_OP_ATTENTION 1  /* n = ns, total = total_q, max_q, heads_q */
+
+/* Bytes of device workspace; (size_t)-1 for unsupported arguments. */
+TQ_API size_t tq_kv8_workspace_bytes(int op, const tq_kv8_t *c, int n, int64_t total, int max_q,
+                                     int heads_q);
+
+/* ---- pages.  All four run on the device alone (no host copy, capturable in a
+ * graph), give the same result every time (pages are taken in ascending
+ * order), and do all or nothing: on an error found on the device they change
+ * nothing and leave the status in the first 4 bytes of d_ws
+ * (tq_device_status): TQ_ERR_ARG for a slot out of range or twice in a list, a
+ * negative count, a length beyond max_pages * page, a fork onto a slot that
+ * holds pages or onto a parent of the same list; TQ_ERR_PAGES when too few
+ * pages are free.  n = 0 is a no-op.  n <= 4096, else TQ_ERR_UNSUPPORTED.
+ * d_ws: >= tq_kv8_workspace_bytes(TQ_KV8_OP_PAGES, c, n, 0, 0, 0).
+ * The tables are taken as these calls leave them; entries out of range are
+ * skipped. */
+
+/* Makes room for d_counts[i] more tokens in slot d_slots[i] and adds them to
+ * its length (the tokens are then written by tq_kv8_append, layer by layer).
+ * Where the first new token falls into a page that another slot holds too, the
+ * slot gets a copy of that page first (all layers, codes and scales). */
+TQ_API int tq_kv8_reserve(const tq_kv8_t *c, int n, const int32_t *d_slots,
+                          const int32_t *d_counts, void *d_ws, size_t ws_bytes, void *stream);
+
+/* Slot d_children[i] (which must hold nothing) becomes a copy of slot
+ * d_parents[i]: same pages, each counted once more; nothing is copied.  A
+ * parent may appear several times. */
+TQ_API int tq_kv8_fork(const tq_kv8_t *c, int n, const int32_t *d_parents,
+                       const int32_t *d_children, void *d_ws, size_t ws_bytes, void *stream);
+
+/* Slot d_slots[i] keeps its first min(d_lens[i], length) tokens and gives up
+ * the pages behind them (0: all of them, the slot is free again). */
+TQ_API int tq_kv8_truncate(const tq_kv8_t *c, int n, const int32_t *d_slots,
+                           const int32_t *d_lens, void *d_ws, size_t ws_bytes, void *stream);
+
+/* Moves the live pages to the front of the pool: with L pages in use, the k-th
+ * page >= L in use moves into the k-th free page < L (all layers), and the
+ * tables and counts follow. */
+TQ_API int tq_kv8_compact(const tq_kv8_t *c, void *d_ws, size_t ws_bytes, void *stream);
+
+/* ---- tokens.  A batch names ns slots (d_slots, or NULL: slots 0 .. ns - 1)
+ * with cu[i+1] - cu[i] tokens each (cu: [ns + 1] on the device, ascending from
+ * 0, at most max_new / max_q tokens a slot).  Slots out of range and table
+ * entries that name no page are passed over: their tokens are not written, read
+ * as 0 and not attended to. */
+
+/* Writes the last cu[i+1] - cu[i] tokens of every slot's length (as
+ * tq_kv8_reserve left it) into the pages of one layer.  d_k, d_v: [total][heads][d]
+ * of x_dtype (TQ_F32, TQ_BF16, TQ_F16), strides in elements.  With r (may be
+ * NULL) the keys are turned to their positions on the way, unrounded.  For
+ * every page and head: s = max(s0, max|x| / M), s0 the scale of the tokens that
+ * the page holds already (if any) and M = 127 or 448; codes = x / s rounded to
+ * nearest even; where s > s0 the codes there are rounded again for s.  NaN
+ * counts as 0, a magnitude above 2^127 (an infinity) as 2^127.  A slot given twice, or slots
+ * that share a page to be written (tq_kv8_reserve leaves none), is not
+ * supported: the page's contents are then undefined. */
+TQ_API int tq_kv8_append(const tq_kv8_t *c, int layer, int ns, const int32_t *d_slots,
+                         const int32_t *d_cu, int64_t total, int max_new, const void *d_k,
+                         const void *d_v, int x_dtype, int64_t x_ts, int64_t x_hs,
+                         const tq_rope_params_t *r, void *stream);
+
+/* Reads tokens d_begin[i] .. d_begin[i] + cu[i+1] - cu[i] of every slot back:
+ * d_k, d_v [total][heads][d] of dtype (either may be NULL), 0 beyond the slot's
+ * length or before its start. */
+TQ_API int tq_kv8_read(const tq_kv8_t *c, int layer, int ns, const int32_t *d_slots,
+                       const int32_t *d_begin, const int32_t *d_cu, int64_t total, int max_new,
+                       void *d_k, void *d_v, int dtype, void *stream);
+
+/* Attention of the last cu[i+1] - cu[i] tokens of every slot over its cached
+ * tokens (one layer).  Query t of n_q sits at position P = length - n_q + t and
+ * sees keys j <= P (causal), and of those j > P - window where window > 0
+ * (causal only); causal = 0: all keys.  Query head h reads KV head
+ * h / (heads_q / heads):
+ *   l_j = scale <q, k_j>,  out = sum_j softmax(l)_j v_j,  lse = log sum_j e^l_j;
+ * a row that sees no key: out = 0, lse = -infinity.
+ * d_q, d_out: [total_q][heads_q][d] of q_dtype (TQ_BF16 or TQ_F16); q with
+ * strides in elements (multiples of 8, the base 16-byte aligned), out
+ * contiguous.  d_lse: [total_q][heads_q] fp32 or NULL.  heads_q a multiple of
+ * heads, at most 128 times as many (else TQ_ERR_UNSUPPORTED).
+ * d_ws: >= tq_kv8_workspace_bytes(TQ_KV8_OP_ATTENTION, c, ns, total_q, max_q,
+ * heads_q); calls that overlap on the GPU need workspaces of their own.  The
+ * result does not depend on what else runs, nor on earlier calls. */
+TQ_API int tq_kv8_attention(const tq_kv8_t *c, int layer, int ns, const int32_t *d_slots,
+                            const int32_t *d_cu, int64_t total_q, int max_q, int heads_q,
+                            const void *d_q, int q_dtype, int64_t q_ts, int64_t q_hs, float scale,
+                            int causal, int window, void *d_out, float *d_lse, void *d_ws,
+                            size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

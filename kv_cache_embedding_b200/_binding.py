@@ -19,10 +19,12 @@ TQ_ERR_CUDA = -4
 TQ_ERR_DEVICE_TIMEOUT = -5
 TQ_ERR_MISMATCH = -6
 TQ_ERR_SCRATCH_LIMIT = -7
+TQ_ERR_PAGES = -8
 TQ_NOALLOC_SCRATCH_BYTES = 8 << 20
 
 TQ_F32 = 0
 TQ_BF16 = 1
+TQ_F16 = 2
 TQ_VARIANT_PROD = 0
 TQ_VARIANT_MSE = 1
 
@@ -34,7 +36,14 @@ EXPORTS = ("tq_workspace_bytes", "tq_status_str", "tq_build_codebook", "tq_build
            "tq_encode", "tq_score",
            "tq_topk", "tq_decode", "tq_logits_fp32", "tq_exact_topk", "tq_topk_noalloc",
            "tq_device_status", "tq_selftest_wait_timeout", "tq_attention_decode",
-           "tq_topk_merge", "tq_score_topk")
+           "tq_topk_merge", "tq_score_topk", "tq_build_rope", "tq_rope",
+           "tq_kv8_workspace_bytes", "tq_kv8_reserve", "tq_kv8_fork", "tq_kv8_truncate",
+           "tq_kv8_compact", "tq_kv8_append", "tq_kv8_read", "tq_kv8_attention")
+
+TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
+TQ_ROPE_PLAIN, TQ_ROPE_LINEAR, TQ_ROPE_NTK, TQ_ROPE_PARTS = range(4)
+TQ_KV_I8, TQ_KV_E4M3 = 0, 1
+TQ_KV8_OP_PAGES, TQ_KV8_OP_ATTENTION = 0, 1
 
 
 class tq_codebook_t(C.Structure):
@@ -53,6 +62,36 @@ class tq_codebook_t(C.Structure):
         ("levels_lo", C.c_int32),
         ("centroids_lo", C.c_float * 16),
         ("boundaries_lo", C.c_float * 16),
+    ]
+
+
+class tq_rope_params_t(C.Structure):
+    _fields_ = [
+        ("d", C.c_int32),
+        ("rot", C.c_int32),
+        ("layout", C.c_int32),
+        ("amplitude", C.c_float),
+        ("turns", C.c_uint64 * 128),
+    ]
+
+
+class tq_kv8_t(C.Structure):
+    _fields_ = [
+        ("d", C.c_int32),
+        ("heads", C.c_int32),
+        ("page", C.c_int32),
+        ("format", C.c_int32),
+        ("layers", C.c_int32),
+        ("slots", C.c_int32),
+        ("max_pages", C.c_int32),
+        ("pages", C.c_int32),
+        ("d_k", C.c_void_p),
+        ("d_v", C.c_void_p),
+        ("d_kscale", C.c_void_p),
+        ("d_vscale", C.c_void_p),
+        ("d_table", C.c_void_p),
+        ("d_len", C.c_void_p),
+        ("d_refs", C.c_void_p),
     ]
 
 
@@ -104,6 +143,25 @@ def _load():
     L.tq_attention_decode.restype = i32
     L.tq_attention_decode.argtypes = [cbp, P, P, cbp, P, i32, i64, P, P, P, P, P, i32, P, i32,
                                       C.c_float, P, P, sz, P]
+    rp, kp, f64 = C.POINTER(tq_rope_params_t), C.POINTER(tq_kv8_t), C.c_double
+    L.tq_build_rope.restype = i32
+    L.tq_build_rope.argtypes = [i32, i32, f64, i32, i32, f64, f64, f64, f64, f64, rp]
+    L.tq_rope.restype = i32
+    L.tq_rope.argtypes = [rp, i64, i32, P, i64, i64, i32, P, P, i64, i64, i32, P]
+    L.tq_kv8_workspace_bytes.restype = sz
+    L.tq_kv8_workspace_bytes.argtypes = [i32, kp, i32, i64, i32, i32]
+    for fn in (L.tq_kv8_reserve, L.tq_kv8_fork, L.tq_kv8_truncate):
+        fn.restype = i32
+        fn.argtypes = [kp, i32, P, P, P, sz, P]
+    L.tq_kv8_compact.restype = i32
+    L.tq_kv8_compact.argtypes = [kp, P, sz, P]
+    L.tq_kv8_append.restype = i32
+    L.tq_kv8_append.argtypes = [kp, i32, i32, P, P, i64, i32, P, P, i32, i64, i64, rp, P]
+    L.tq_kv8_read.restype = i32
+    L.tq_kv8_read.argtypes = [kp, i32, i32, P, P, P, i64, i32, P, P, i32, P]
+    L.tq_kv8_attention.restype = i32
+    L.tq_kv8_attention.argtypes = [kp, i32, i32, P, P, i64, i32, i32, P, i32, i64, i64, C.c_float,
+                                   i32, i32, P, P, P, sz, P]
     return L
 
 
@@ -212,3 +270,57 @@ def tq_score_topk(cb, d_Pi, d_S, G, n, d_codes, d_xnorm, d_rnorm, nq, d_q, q_dty
                lib.tq_score_topk(C.byref(cb), d_Pi, d_S, G, n, d_codes, d_xnorm, d_rnorm, nq, d_q,
                                  q_dtype, k, d_scores, d_vals, d_ids, d_ws, ws_bytes, stream))
 
+
+def tq_build_rope(d, rot, base, layout, scaling, factor, ctx, low, high, amplitude, r):
+    return _ok("tq_build_rope", lib.tq_build_rope(d, rot, base, layout, scaling, factor, ctx, low,
+                                                  high, amplitude, C.byref(r)))
+
+
+def tq_rope(r, T, heads, d_x, x_ts, x_hs, x_dtype, d_pos, d_out, out_ts, out_hs, transpose,
+            stream):
+    return _ok("tq_rope", lib.tq_rope(C.byref(r), T, heads, d_x, x_ts, x_hs, x_dtype, d_pos, d_out,
+                                      out_ts, out_hs, transpose, stream))
+
+
+def tq_kv8_workspace_bytes(op, c, n, total, max_q, heads_q):
+    return int(lib.tq_kv8_workspace_bytes(op, C.byref(c), n, total, max_q, heads_q))
+
+
+def tq_kv8_reserve(c, n, d_slots, d_counts, d_ws, ws_bytes, stream):
+    return _ok("tq_kv8_reserve", lib.tq_kv8_reserve(C.byref(c), n, d_slots, d_counts, d_ws,
+                                                    ws_bytes, stream))
+
+
+def tq_kv8_fork(c, n, d_parents, d_children, d_ws, ws_bytes, stream):
+    return _ok("tq_kv8_fork", lib.tq_kv8_fork(C.byref(c), n, d_parents, d_children, d_ws, ws_bytes,
+                                              stream))
+
+
+def tq_kv8_truncate(c, n, d_slots, d_lens, d_ws, ws_bytes, stream):
+    return _ok("tq_kv8_truncate", lib.tq_kv8_truncate(C.byref(c), n, d_slots, d_lens, d_ws,
+                                                      ws_bytes, stream))
+
+
+def tq_kv8_compact(c, d_ws, ws_bytes, stream):
+    return _ok("tq_kv8_compact", lib.tq_kv8_compact(C.byref(c), d_ws, ws_bytes, stream))
+
+
+def tq_kv8_append(c, layer, ns, d_slots, d_cu, total, max_new, d_k, d_v, x_dtype, x_ts, x_hs, r,
+                  stream):
+    """r: a tq_rope_params_t, or None."""
+    return _ok("tq_kv8_append", lib.tq_kv8_append(C.byref(c), layer, ns, d_slots, d_cu, total,
+                                                  max_new, d_k, d_v, x_dtype, x_ts, x_hs,
+                                                  C.byref(r) if r is not None else None, stream))
+
+
+def tq_kv8_read(c, layer, ns, d_slots, d_begin, d_cu, total, max_new, d_k, d_v, dtype, stream):
+    return _ok("tq_kv8_read", lib.tq_kv8_read(C.byref(c), layer, ns, d_slots, d_begin, d_cu, total,
+                                              max_new, d_k, d_v, dtype, stream))
+
+
+def tq_kv8_attention(c, layer, ns, d_slots, d_cu, total_q, max_q, heads_q, d_q, q_dtype, q_ts,
+                     q_hs, scale, causal, window, d_out, d_lse, d_ws, ws_bytes, stream):
+    return _ok("tq_kv8_attention",
+               lib.tq_kv8_attention(C.byref(c), layer, ns, d_slots, d_cu, total_q, max_q, heads_q,
+                                    d_q, q_dtype, q_ts, q_hs, scale, causal, window, d_out, d_lse,
+                                    d_ws, ws_bytes, stream))

@@ -13,6 +13,7 @@ extern "C" const char* tq_status_str(int status) {
         case TQ_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
         case TQ_ERR_MISMATCH: return "codebook does not match the call";
         case TQ_ERR_SCRATCH_LIMIT: return "sizes need more scratch than tq_topk_noalloc's fixed 8 MiB array";
+        case TQ_ERR_PAGES: return "not enough free pages in the cache";
         default: return "unknown status";
     }
 }
@@ -82,5 +83,6 @@ extern "C" int tq_device_status(const void* d_ws, void* stream) {
     cudaStream_t s = (cudaStream_t)stream;
     TQ_TRY_CUDA(cudaMemcpyAsync(&word, d_ws, sizeof(int), cudaMemcpyDeviceToHost, s));
     TQ_TRY_CUDA(cudaStreamSynchronize(s));
+    if (word == TQ_ERR_ARG || word == TQ_ERR_PAGES) return word;  // a page operation's refusal
     return word == 0 ? TQ_OK : TQ_ERR_DEVICE_TIMEOUT;
 }

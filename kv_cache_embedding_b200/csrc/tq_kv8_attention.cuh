@@ -1,0 +1,69 @@
+// Attention over the 8-bit paged cache: what its kernels share.
+#pragma once
+
+#include <cuda.h>
+
+#include "tq_kv8.cuh"
+#include "tq_sm100.cuh"
+
+namespace tq {
+namespace kv8 {
+
+// One call (kernel parameter).
+struct Attn {
+    View v;
+    int ns, group, heads_q, causal, window;
+    const int32_t* slots;
+    const int32_t* cu;
+    int64_t total_q;
+    const void* q;
+    int64_t q_ts, q_hs;
+    float scale_log2;  // scale * log2(e)
+    const float *ks, *vs;  // [pages][heads] of the layer
+    void* out;
+    float* lse;
+    int rows;  // rows of the layer's pools: pages * heads * page
+};
+
+// A batch entry as the kernels see it.
+struct Entry {
+    int slot, len, qn;
+    int64_t c0;  // first query token
+};
+__device__ __forceinline__ Entry entry_of(const Attn& a, int i) {
+    Entry e;
+    e.slot = slot_of(a.v, a.slots, i);
+    const int64_t c0 = a.cu[i], c1 = min((int64_t)a.cu[i + 1], a.total_q);
+    e.c0 = c0;
+    e.qn = c0 >= 0 && c1 > c0 ? (int)(c1 - c0) : 0;
+    e.len = e.slot >= 0 ? length_of(a.v, e.slot) : 0;
+    return e;
+}
+// First key that any query of the entry sees.
+__device__ __forceinline__ int first_key(const Attn& a, const Entry& e) {
+    return a.window > 0 ? max(0, e.len - e.qn - a.window + 1) : 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The power of two that brings a row's largest magnitude into [1, 2): with it a
+// 16-bit row is a row of halves, exact down to 2^-14 of the largest and within
+// 2^-25 of it below.
+__device__ __forceinline__ float row_unit(float top) {
+    int e = (int)(__float_as_uint(top) >> 23);
+    e = min(max(e, 1), 253);
+    return __uint_as_float((uint32_t)(254 - e) << 23);
+}
+
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+// Tensor map of a layer's code rows: [pages * heads * page][d] bytes, boxes of
+// `box` rows, swizzled over a whole row (128 or 64 bytes).
+int code_map(CUtensorMap* m, const void* base, int d, int64_t rows, int box);
+
+}  // namespace kv8
+}  // namespace tq

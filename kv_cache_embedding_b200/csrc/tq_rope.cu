@@ -1,0 +1,189 @@
+// Rotary positions: for token t, head h and each pair (x1, x2) of the first
+// `rot` coordinates, with angle p f_i at position p,
+//   y1 = a (x1 cos - x2 sin),   y2 = a (x2 cos + x1 sin)
+// (transposed: sin -> -sin), the coordinates behind copied.
+//
+// One pass over the data: a block takes whole tokens, forms their rot/2 cosines
+// and sines once in shared memory (all heads of a token share them; no table in
+// global memory, no limit on the position) and turns the heads with 16-byte
+// accesses where strides and widths allow them.  Bound by HBM for many tokens,
+// by the launch for few.
+#include <cmath>
+
+#include "tq_internal.cuh"
+#include "tq_rope.cuh"
+
+namespace tq {
+
+bool rope_valid(const tq_rope_params_t* r) {
+    return r && r->d >= 2 && r->d <= 256 && r->d % 2 == 0 && r->rot >= 0 && r->rot <= r->d &&
+           r->rot % 2 == 0 && (r->layout == TQ_ROPE_HALF || r->layout == TQ_ROPE_INTERLEAVED);
+}
+
+namespace {
+
+constexpr int kRT = 256;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ void from_f(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_f(float v, __half& o) { o = __float2half_rn(v); }
+
+template <typename T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+    T v[VEC];
+};
+
+// VEC: elements per access (16 bytes, or 1).  An item is two runs of VEC
+// elements for the half layout's pairs (i, i + rot/2), one run otherwise; with
+// VEC = 1 an interleaved pair is two runs of one.
+template <typename T, int VEC>
+__global__ __launch_bounds__(kRT) void k_rope(const __grid_constant__ tq_rope_params_t r, int64_t T_,
+                                              int heads, const T* __restrict__ x, int64_t x_ts,
+                                              int64_t x_hs, const int64_t* __restrict__ pos, T* out,
+                                              int64_t out_ts, int64_t out_hs, int transpose,
+                                              int tokens, int in_place) {
+    extern __shared__ float2 s_cs[];  // [tokens][rot/2]: a cos, a sin
+    using P = Pack<T, VEC>;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int nt = (int)min((int64_t)tokens, T_ - t0);
+    const int half = r.rot / 2;
+    for (int i = threadIdx.x; i < nt * half; i += kRT) {
+        const int t = i / half, m = i - t * half;
+        float c, s;
+        rope_angle(r.turns[m], pos[t0 + t], c, s);
+        s_cs[i] = make_float2(c * r.amplitude, (transpose ? -s : s) * r.amplitude);
+    }
+    __syncthreads();
+    const bool split = r.layout == TQ_ROPE_HALF || VEC == 1;  // items of two runs
+    const int turned = split ? half / VEC : r.rot / VEC;
+    const int items = turned + (in_place ? 0 : (r.d - r.rot) / VEC);
+    const int per = heads * items;
+    for (int i = threadIdx.x; i < nt * per; i += kRT) {
+        const int t = i / per, hi = i - t * per;
+        const int h = hi / items, it = hi - h * items;
+        const T* xr = x + (t0 + t) * x_ts + h * x_hs;
+        T* orow = out + (t0 + t) * out_ts + h * out_hs;
+        const float2* cs = s_cs + t * half;
+        if (it >= turned) {
+            const int o = r.rot + (it - turned) * VEC;
+            *reinterpret_cast<P*>(orow + o) = *reinterpret_cast<const P*>(xr + o);
+        } else if (split) {
+            const int m = it * VEC;
+            const int o1 = r.layout == TQ_ROPE_HALF ? m : 2 * m;
+            const int o2 = r.layout == TQ_ROPE_HALF ? m + half : 2 * m + 1;
+            P a = *reinterpret_cast<const P*>(xr + o1);
+            P b = *reinterpret_cast<const P*>(xr + o2);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float x1 = to_f(a.v[e]), x2 = to_f(b.v[e]);
+                const float2 w = cs[m + e];
+                from_f(x1 * w.x - x2 * w.y, a.v[e]);
+                from_f(x2 * w.x + x1 * w.y, b.v[e]);
+            }
+            *reinterpret_cast<P*>(orow + o1) = a;
+            *reinterpret_cast<P*>(orow + o2) = b;
+        } else {
+            P a = *reinterpret_cast<const P*>(xr + it * VEC);
+#pragma unroll
+            for (int e = 0; e + 1 < VEC; e += 2) {
+                const float x1 = to_f(a.v[e]), x2 = to_f(a.v[e + 1]);
+                const float2 w = cs[(it * VEC + e) / 2];
+                from_f(x1 * w.x - x2 * w.y, a.v[e]);
+                from_f(x2 * w.x + x1 * w.y, a.v[e + 1]);
+            }
+            *reinterpret_cast<P*>(orow + it * VEC) = a;
+        }
+    }
+}
+
+template <typename T>
+int launch(const tq_rope_params_t& r, int64_t T_, int heads, const void* x, int64_t x_ts,
+           int64_t x_hs, const int64_t* pos, void* out, int64_t out_ts, int64_t out_hs,
+           int transpose, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const bool wide = r.d % V == 0 && (r.layout == TQ_ROPE_HALF ? r.rot / 2 : r.rot) % V == 0 &&
+                      ((uintptr_t)x | (uintptr_t)out) % 16 == 0 && x_ts % V == 0 && x_hs % V == 0 &&
+                      out_ts % V == 0 && out_hs % V == 0;
+    const int in_place = x == out;
+    // about two accesses a thread and block: whole tokens, one at least
+    const int per = heads * (wide ? r.d / V : r.d);
+    int tokens = per >= 2 * kRT ? 1 : (2 * kRT + per - 1) / per;
+    if (tokens > 16) tokens = 16;
+    const int64_t blocks = (T_ + tokens - 1) / tokens;
+    if (blocks > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
+    const size_t smem = (size_t)tokens * (r.rot / 2) * sizeof(float2);
+    if (wide)
+        k_rope<T, V><<<(unsigned)blocks, kRT, smem, s>>>(r, T_, heads, (const T*)x, x_ts, x_hs, pos,
+                                                         (T*)out, out_ts, out_hs, transpose, tokens,
+                                                         in_place);
+    else
+        k_rope<T, 1><<<(unsigned)blocks, kRT, smem, s>>>(r, T_, heads, (const T*)x, x_ts, x_hs, pos,
+                                                         (T*)out, out_ts, out_hs, transpose, tokens,
+                                                         in_place);
+    TQ_CHECK_LAUNCH();
+    return TQ_OK;
+}
+
+}  // namespace
+}  // namespace tq
+
+using namespace tq;
+
+extern "C" int tq_build_rope(int d, int rot, double base, int layout, int scaling, double factor,
+                             double ctx, double low, double high, double amplitude,
+                             tq_rope_params_t* r) {
+    if (!r || (layout != TQ_ROPE_HALF && layout != TQ_ROPE_INTERLEAVED)) return TQ_ERR_ARG;
+    if (scaling < TQ_ROPE_PLAIN || scaling > TQ_ROPE_PARTS) return TQ_ERR_ARG;
+    if (d < 2 || d > 256 || d % 2 || rot < 0 || rot > d || rot % 2) return TQ_ERR_UNSUPPORTED;
+    if (!std::isfinite(base) || base <= 1.0 || !std::isfinite(amplitude) ||
+        !std::isfinite((float)amplitude))
+        return TQ_ERR_ARG;
+    if (scaling != TQ_ROPE_PLAIN && (!std::isfinite(factor) || factor < 1.0)) return TQ_ERR_ARG;
+    if (scaling == TQ_ROPE_NTK && rot < 4) return TQ_ERR_UNSUPPORTED;
+    if (scaling == TQ_ROPE_PARTS && (!std::isfinite(ctx) || ctx <= 0.0 || !std::isfinite(low) ||
+                                     !std::isfinite(high) || low >= high))
+        return TQ_ERR_ARG;
+    const double two_pi = 6.283185307179586476925;
+    tq_rope_params_t p = {};
+    p.d = d;
+    p.rot = rot;
+    p.layout = layout;
+    p.amplitude = (float)amplitude;
+    if (scaling == TQ_ROPE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
+    if (!std::isfinite(base)) return TQ_ERR_ARG;
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot);
+        if (scaling == TQ_ROPE_LINEAR) f /= factor;
+        if (scaling == TQ_ROPE_PARTS) {
+            double g = (ctx * f / two_pi - low) / (high - low);
+            g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
+            f *= g + (1.0 - g) / factor;
+        }
+        // 0 < f <= 1 radian: below 1/6 turn; 2^64 times it keeps fp64's precision
+        p.turns[i] = (uint64_t)std::llrint(std::ldexp(f / two_pi, 63)) << 1;
+    }
+    *r = p;
+    return TQ_OK;
+}
+
+extern "C" int tq_rope(const tq_rope_params_t* r, int64_t T, int heads, const void* d_x,
+                       int64_t x_ts, int64_t x_hs, int x_dtype, const int64_t* d_pos, void* d_out,
+                       int64_t out_ts, int64_t out_hs, int transpose, void* stream) {
+    if (!r || T < 0 || heads < 1 || transpose < 0 || transpose > 1) return TQ_ERR_ARG;
+    if (x_dtype != TQ_F32 && x_dtype != TQ_BF16 && x_dtype != TQ_F16) return TQ_ERR_ARG;
+    if (!rope_valid(r)) return TQ_ERR_ARG;
+    if (T == 0) return TQ_OK;
+    if (!d_x || !d_pos || !d_out) return TQ_ERR_ARG;
+    if (d_x == d_out && (x_ts != out_ts || x_hs != out_hs)) return TQ_ERR_ARG;
+    // a block indexes its tokens' heads in 32 bits
+    if ((int64_t)heads * r->d > ((int64_t)1 << 26)) return TQ_ERR_UNSUPPORTED;
+    cudaStream_t s = (cudaStream_t)stream;
+    switch (x_dtype) {
+        case TQ_F32: return launch<float>(*r, T, heads, d_x, x_ts, x_hs, d_pos, d_out, out_ts, out_hs, transpose, s);
+        case TQ_BF16: return launch<__nv_bfloat16>(*r, T, heads, d_x, x_ts, x_hs, d_pos, d_out, out_ts, out_hs, transpose, s);
+        default: return launch<__half>(*r, T, heads, d_x, x_ts, x_hs, d_pos, d_out, out_ts, out_hs, transpose, s);
+    }
+}
