@@ -10,7 +10,7 @@
 //
 // Work.  Reading the cache is the cost (2 d bytes a token and KV head for up to
 // 16 rows), so every warp is a stream of its own: it takes an equal, contiguous
-// share of all (entry, head, 16-row group, 32-key tile) steps of the batch --
+// share of all (entry, head, 32-key tile) steps of the batch --
 // ragged lengths included -- and keeps kStages tiles of K and V in flight by TMA
 // into its private ring; warps meet only where an item's steps are cut, and
 // there k_attn_merge joins the parts in the order of their keys.  Products are
@@ -66,13 +66,6 @@ constexpr int kThreads = 32 * kWarps;
 // Workspace: [status word (256 B) | a status word a block | a Cut a warp | per
 // warp two parts: (m, L) of 16 rows, 16 x d sums].  Part 2u: the end of an item
 // that warp u did not begin; 2u + 1: the beginning of one that it does not end.
-struct Cut {
-    int parts;       // warps that share the item which begins here; 0: none
-    int rows, head;  // its rows (1..16) and KV head
-    int pad;
-    int64_t row0;    // its first row of the entry's (token x group) rows, from token 0
-};
-
 struct Parts {
     int* status;
     int* block_status;
@@ -126,42 +119,36 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
                     : (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
 }
 
-// Steps of batch entry i: heads x row groups x tiles (one tile at least, so that
-// rows without keys are written).
+// Steps of batch entry i: heads x tiles (one tile at least, so that rows without
+// keys are written); none where it has no rows, or too many for this kernel.
 struct Span {
     Entry e;
-    int groups, tile0, tiles;
+    int tile0, tiles;
     int64_t steps;
 };
 __device__ __forceinline__ Span span_of(const Attn& a, int i) {
     Span s;
     s.e = entry_of(a, i);
-    s.groups = (int)(((int64_t)s.e.qn * a.group + kRows - 1) / kRows);
     s.tile0 = first_key(a, s.e) / kTile;
     s.tiles = max(1, (s.e.len + kTile - 1) / kTile - s.tile0);
-    s.steps = (int64_t)a.v.heads * s.groups * s.tiles;
+    const int64_t rows = (int64_t)s.e.qn * a.group;
+    s.steps = rows > 0 && rows <= a.few ? (int64_t)a.v.heads * s.tiles : 0;
     return s;
 }
 
 // Where step g lies.
 struct Place {
     Span s;
-    int entry, head, grp, t;  // t: tile within the item
+    int entry, head, t;  // t: tile within the item
     __device__ __forceinline__ void open(int64_t rem) {
-        const int64_t item = rem / s.tiles;
-        t = (int)(rem - item * s.tiles);
-        head = (int)(item / s.groups);
-        grp = (int)(item - (int64_t)head * s.groups);
+        head = (int)(rem / s.tiles);
+        t = (int)(rem - (int64_t)head * s.tiles);
     }
-    // the next step; g: its number, pre: unused where the entry goes on
-    __device__ __forceinline__ bool next() {  // false: the entry is through
+    __device__ __forceinline__ bool next(int heads) {  // false: the entry is through
         if (++t < s.tiles) return true;
         t = 0;
-        if (++grp < s.groups) return true;
-        grp = 0;
-        return ++head < a_heads;
+        return ++head < heads;
     }
-    int a_heads;
 };
 
 template <int FMT, int D, typename T>
@@ -226,7 +213,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             ++i;
         }
         p.entry = i;
-        p.a_heads = a.v.heads;
         p.open(rem);
     };
 
@@ -265,15 +251,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         }
         pend_stage = pstage;
         pstage = pstage + 1 == kStages ? 0 : pstage + 1;
-        if (++gp < g1 && !pp.next()) {
+        if (++gp < g1 && !pp.next(a.v.heads)) {
             // the following entry with steps
-            int64_t rem = 0;
             int i = pp.entry;
             do {
                 pp.s = span_of(a, ++i);
             } while (pp.s.steps == 0);
             pp.entry = i;
-            pp.open(rem);
+            pp.open(0);
         }
     };
 
@@ -297,8 +282,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         const int t_begin = p.t;
         const int t_end = (int)min((int64_t)p.s.tiles, t_begin + left);
         const Entry e = p.s.e;
-        const int64_t row_first = (int64_t)p.grp * kRows;
-        const int nrows = (int)min((int64_t)kRows, (int64_t)e.qn * a.group - row_first);
+        const int nrows = e.qn * a.group;
         // rows r0 and r0 + 8 of this thread: query token, and the last key it sees
         uint32_t qf[CH][4];
         float sl[2], m[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
@@ -306,12 +290,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int r = r0 + 8 * u;
-            const int64_t ri = row_first + min(r, nrows - 1);
-            const int tq = (int)(ri / a.group), hq = (int)(ri - (int64_t)tq * a.group);
+            const int ri = min(r, nrows - 1), tq = ri / a.group, hq = ri - tq * a.group;
             const T* q = (const T*)a.q + (e.c0 + tq) * a.q_ts + (int64_t)(p.head * a.group + hq) * a.q_hs;
             const int pos = e.len - e.qn + tq;
             lim[u] = a.causal ? min(pos, e.len - 1) : e.len - 1;
-            low[u] = a.window > 0 ? pos - a.window : -1;
+            low[u] = below_window(a, pos);
             float x[CH][4], top = 0.f;
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
@@ -333,10 +316,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             }
         }
         // keys below `clear` and above `low_any` need no mask for any row
-        const int first_tok = (int)(row_first / a.group);
-        const int last_tok = (int)((row_first + nrows - 1) / a.group);
-        const int clear = a.causal ? min(e.len - e.qn + first_tok, e.len - 1) : e.len - 1;
-        const int low_any = a.window > 0 ? e.len - e.qn + last_tok - a.window : -1;
+        const int clear = a.causal ? min(e.len - e.qn, e.len - 1) : e.len - 1;
+        const int low_any = a.window > 0 ? e.len - 1 - a.window : -1;
         float o[2 * CH][4];  // chunk, parity: coordinates 16 ch + 4 c2 + 2 {0, 1} + parity
 #pragma unroll
         for (int i = 0; i < 2 * CH; ++i)
@@ -473,9 +454,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             for (int u = 0; u < 2; ++u) {
                 const int r = r0 + 8 * u;
                 if (r >= nrows) continue;
-                const int64_t ri = row_first + r;
-                const int64_t tok = e.c0 + ri / a.group;
-                const int hq = p.head * a.group + (int)(ri % a.group);
+                const int64_t tok = e.c0 + r / a.group;
+                const int hq = p.head * a.group + r % a.group;
                 const float n = L[u] > 0.f ? R / L[u] : (L[u] == 0.f ? 0.f : L[u]);
                 T* out = (T*)a.out + (tok * a.heads_q + hq) * D;
 #pragma unroll
@@ -511,14 +491,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                 c.rows = nrows;
                 c.head = p.head;
                 c.pad = 0;
-                c.row0 = e.c0 * a.group + row_first;
+                c.row0 = e.c0 * a.group;
                 parts.cut[unit] = c;
             }
         }
         g += t_end - t_begin;
         if (g < g1) {
             p.t = p.s.tiles - 1;
-            if (!p.next()) {
+            if (!p.next(a.v.heads)) {
                 int i = p.entry;
                 do {
                     p.s = span_of(a, ++i);
@@ -599,13 +579,23 @@ constexpr int kMaxBlocks = 148;  // the workspace's size
 
 // The most steps that a call of these sizes can have (its lengths lie on the
 // device); blocks: one an SM, fewer where the tables are too short to fill them.
-int64_t most_steps(const tq_kv8_t* c, int ns, int64_t total_q, int heads_q) {
-    const int64_t tiles = ((int64_t)c->max_pages * c->page + kTile - 1) / kTile;
-    return tiles * (total_q * (heads_q / c->heads) / kRows + ns) * c->heads;
+int64_t most_steps(const tq_kv8_t* c, int ns) {
+    return ((int64_t)c->max_pages * c->page + kTile - 1) / kTile * ns * c->heads;
 }
-int64_t blocks_for(const tq_kv8_t* c, int ns, int64_t total_q, int heads_q) {
-    const int64_t steps = most_steps(c, ns, total_q, heads_q);
+int64_t blocks_for(const tq_kv8_t* c, int ns) {
+    const int64_t steps = most_steps(c, ns);
     return steps < kMaxBlocks ? (steps < 1 ? 1 : steps) : kMaxBlocks;
+}
+
+// Which kernels a call launches: an entry of up to kRows rows takes the few-rows
+// kernel.  The counts of a batch lie on the device; where total_q is ns times
+// max_q every entry has max_q tokens (or the batch is padded), and beyond kRows
+// the prompt kernel takes all entries.
+bool any_few(const tq_kv8_t* c, int ns, int64_t total_q, int max_q, int heads_q) {
+    return (int64_t)max_q * (heads_q / c->heads) <= kRows || total_q < (int64_t)ns * max_q;
+}
+bool any_many(const tq_kv8_t* c, int max_q, int heads_q) {
+    return (int64_t)max_q * (heads_q / c->heads) > kRows;
 }
 
 template <int D>
@@ -642,26 +632,29 @@ int launch(const Attn& a, const CUtensorMap& km, const CUtensorMap& vm, const Pa
 
 template <int D>
 int dispatch(const tq_kv8_t* c, const Attn& a, const CUtensorMap& km, const CUtensorMap& vm,
-             void* ws, size_t ws_bytes, int blocks, int cuts, int rows, int q_dtype, cudaStream_t s) {
-    size_t need;
-    const Parts p = carve<D>(ws, blocks, &need);
-    if (!ws || ws_bytes < need) return TQ_ERR_WORKSPACE;
+             const Parts& p, int blocks, int cuts, int rows, int q_dtype, cudaStream_t s) {
     if (c->format == TQ_KV_I8)
-        return q_dtype == TQ_BF16 ? launch<TQ_KV_I8, D, __nv_bfloat16>(a, km, vm, p, blocks, cuts, rows, s)
-                                  : launch<TQ_KV_I8, D, __half>(a, km, vm, p, blocks, cuts, rows, s);
-    return q_dtype == TQ_BF16 ? launch<TQ_KV_E4M3, D, __nv_bfloat16>(a, km, vm, p, blocks, cuts, rows, s)
-                              : launch<TQ_KV_E4M3, D, __half>(a, km, vm, p, blocks, cuts, rows, s);
+        return q_dtype == TQ_BF16
+                   ? launch<TQ_KV_I8, D, __nv_bfloat16>(a, km, vm, p, blocks, cuts, rows, s)
+                   : launch<TQ_KV_I8, D, __half>(a, km, vm, p, blocks, cuts, rows, s);
+    return q_dtype == TQ_BF16
+               ? launch<TQ_KV_E4M3, D, __nv_bfloat16>(a, km, vm, p, blocks, cuts, rows, s)
+               : launch<TQ_KV_E4M3, D, __half>(a, km, vm, p, blocks, cuts, rows, s);
+}
+
+Parts carve_for(const tq_kv8_t* c, void* ws, int64_t blocks, size_t* bytes) {
+    return c->d == 128 ? carve<128>(ws, blocks, bytes) : carve<64>(ws, blocks, bytes);
 }
 
 }  // namespace
 
+// [status word | the few-rows kernel's parts | the prompt kernel's parts]
 size_t attention_workspace(const tq_kv8_t* c, int ns, int64_t total_q, int max_q, int heads_q) {
-    (void)max_q;
-    size_t need;
-    const int64_t blocks = blocks_for(c, ns, total_q, heads_q);
-    if (c->d == 128) carve<128>(nullptr, blocks, &need);
-    else carve<64>(nullptr, blocks, &need);
-    return need;
+    size_t few = 256, many = 0;
+    if (any_few(c, ns, total_q, max_q, heads_q)) carve_for(c, nullptr, blocks_for(c, ns), &few);
+    if (any_many(c, max_q, heads_q))
+        prompt_carve(c, nullptr, prompt_blocks(c, ns, total_q, heads_q), &many);
+    return few + many;
 }
 
 }  // namespace kv8
@@ -686,12 +679,8 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
     if (ns == 0 || total_q == 0 || max_q == 0) return TQ_OK;
     if (!d_cu || !d_q || !d_out || (((uintptr_t)d_q | (uintptr_t)d_out) & 15u) || q_ts % 8 || q_hs % 8)
         return TQ_ERR_ARG;
-    const int64_t rows = (int64_t)c->pages * c->heads * c->page;
-    CUtensorMap km, vm;
-    const int box = c->page < kv8::kTile ? c->page : kv8::kTile;
-    int rc = kv8::code_map(&km, (const char*)c->d_k + layer * kv8::layer_bytes(c), c->d, rows, box);
-    if (!rc) rc = kv8::code_map(&vm, (const char*)c->d_v + layer * kv8::layer_bytes(c), c->d, rows, box);
-    if (rc) return rc;
+    if (!d_ws || ws_bytes < kv8::attention_workspace(c, ns, total_q, max_q, heads_q))
+        return TQ_ERR_WORKSPACE;
     kv8::Attn a;
     a.v = kv8::view(c);
     a.ns = ns;
@@ -710,14 +699,32 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
     a.vs = c->d_vscale + layer * kv8::layer_scales(c);
     a.out = d_out;
     a.lse = d_lse;
-    a.rows = (int)rows;
-    const int blocks = (int)kv8::blocks_for(c, ns, total_q, heads_q);
-    const int64_t steps = kv8::most_steps(c, ns, total_q, heads_q);
-    const int cuts = (int)(steps < blocks * kv8::kWarps ? steps : blocks * kv8::kWarps);
-    const int64_t most = (int64_t)max_q * a.group;
-    const int grp_rows = (int)(most < kv8::kRows ? most : kv8::kRows);
+    a.rows = c->pages * c->heads * c->page;
     cudaStream_t s = (cudaStream_t)stream;
-    return c->d == 128
-               ? kv8::dispatch<128>(c, a, km, vm, d_ws, ws_bytes, blocks, cuts, grp_rows, q_dtype, s)
-               : kv8::dispatch<64>(c, a, km, vm, d_ws, ws_bytes, blocks, cuts, grp_rows, q_dtype, s);
+    const bool few = kv8::any_few(c, ns, total_q, max_q, heads_q);
+    a.few = few ? kv8::kRows : 0;
+    size_t at = 256;
+    if (few) {
+        const int box = c->page < kv8::kTile ? c->page : kv8::kTile;
+        CUtensorMap km, vm;
+        int rc = kv8::code_map(&km, (const char*)c->d_k + layer * kv8::layer_bytes(c), c->d, a.rows, box);
+        if (!rc) rc = kv8::code_map(&vm, (const char*)c->d_v + layer * kv8::layer_bytes(c), c->d, a.rows, box);
+        if (rc) return rc;
+        const int blocks = (int)kv8::blocks_for(c, ns);
+        const kv8::Parts p = kv8::carve_for(c, d_ws, blocks, &at);
+        const int64_t steps = kv8::most_steps(c, ns);
+        const int cuts = (int)(steps < blocks * kv8::kWarps ? steps : blocks * kv8::kWarps);
+        const int64_t most = (int64_t)max_q * a.group;
+        const int rows = (int)(most < kv8::kRows ? most : kv8::kRows);
+        rc = c->d == 128 ? kv8::dispatch<128>(c, a, km, vm, p, blocks, cuts, rows, q_dtype, s)
+                         : kv8::dispatch<64>(c, a, km, vm, p, blocks, cuts, rows, q_dtype, s);
+        if (rc) return rc;
+    }
+    if (!kv8::any_many(c, max_q, heads_q)) return TQ_OK;
+    size_t bytes;
+    const int blocks = kv8::prompt_blocks(c, ns, total_q, heads_q);
+    kv8::PromptParts p = kv8::prompt_carve(c, (char*)d_ws + at, blocks, &bytes);
+    p.status = (int*)d_ws;
+    p.keep_status = few;
+    return kv8::launch_prompt(c, layer, a, p, blocks, q_dtype, s);
 }

@@ -23,7 +23,32 @@ struct Attn {
     void* out;
     float* lse;
     int rows;  // rows of the layer's pools: pages * heads * page
+    int few;   // entries of up to `few` query rows (tokens x group) run on the few-rows
+               // kernel, the others on the prompt kernel (0: all of them)
 };
+
+// An item that its warp (or CTA) begins and others go on with: who joins what.
+struct Cut {
+    int parts;       // streams that share the item which begins here; 0: none
+    int rows, head;  // its rows and KV head
+    int pad;
+    int64_t row0;    // its first row of the entry's (token x group) rows, from token 0
+};
+
+// The prompt kernel's workspace.  Part 2u: the end of an item that CTA u did not
+// begin; 2u + 1: the beginning of one that it does not end.
+struct PromptParts {
+    int* status;
+    int keep_status;   // the few-rows kernel runs before and owns the word
+    int* block_status;
+    Cut* cut;
+    float2* ml;        // (m, L) of 256 rows a part
+    float* o;          // 256 x d a part
+};
+int prompt_blocks(const tq_kv8_t* c, int ns, int64_t total_q, int heads_q);
+PromptParts prompt_carve(const tq_kv8_t* c, void* ws, int blocks, size_t* bytes);
+int launch_prompt(const tq_kv8_t* c, int layer, const Attn& a, const PromptParts& p, int blocks,
+                  int q_dtype, cudaStream_t s);
 
 // A batch entry as the kernels see it.
 struct Entry {
@@ -41,7 +66,11 @@ __device__ __forceinline__ Entry entry_of(const Attn& a, int i) {
 }
 // First key that any query of the entry sees.
 __device__ __forceinline__ int first_key(const Attn& a, const Entry& e) {
-    return a.window > 0 ? max(0, e.len - e.qn - a.window + 1) : 0;
+    return a.window > 0 ? (int)max((int64_t)0, (int64_t)e.len - e.qn - a.window + 1) : 0;
+}
+// The last key that the query at position pos does not see for the window.
+__device__ __forceinline__ int below_window(const Attn& a, int pos) {
+    return a.window > 0 ? (int)max((int64_t)-1, (int64_t)pos - a.window) : -1;
 }
 
 __device__ __forceinline__ float ex2(float x) {

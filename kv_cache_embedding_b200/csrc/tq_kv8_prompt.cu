@@ -1,0 +1,767 @@
+// Attention over the 8-bit paged cache, many query rows (prompts, chunks behind
+// a prefix, drafts): the sums of tq_kv8_attention.cu on the sm_100a tensor cores.
+//
+//   S = Q C_k^T   (rows x 128 keys),   P = 2^(S s_k s_q - m),   O += (P s_v / R) C_v
+//
+// with the codes C as exact halves, Q a row of halves times a power of two, s_k
+// and s_v one number per 16 keys (a page at least), m the row's reference
+// maximum and R the largest s_v of the item's keys; P is rounded to a half once,
+// sums are fp32.
+//
+// A CTA runs items of 256 rows (two stages of 128) of one entry and KV head over
+// tiles of 128 keys; the steps (item x tile) of the whole batch are shared out
+// evenly, contiguously, over one CTA an SM, so ragged and causal batches balance
+// and a long context with few rows fills the machine; the items that are cut are
+// joined by k_prompt_merge.  Warps:
+//   0-3, 4-7  softmax of stage 0, 1: a thread a row.  Loads its query row, turns
+//             S (tensor memory) into P in place, rescales O only when the row's
+//             maximum has grown by more than 2^8 (the reference m then follows;
+//             P <= 2^8 meanwhile, far inside a half's range), writes the result.
+//   8-11      codes -> halves: from the TMA ring (128 keys x d bytes) into the
+//             swizzled operand tiles of K (K-major) and V (the same rows, read
+//             MN-major), with the tile's scales.
+//   12        issues the MMAs: per tile and stage O += P V of this tile, then S of
+//             the next, so each stage's softmax hides behind the other's MMAs.
+//   13        the TMA loads, a page table lookup a box.
+// Every wait is bounded (1 s); a warp that gives up sets the abort flag and the
+// call's status.
+#include "tq_kv8_attention.cuh"
+#include "tq_score_common.cuh"
+
+namespace tq {
+namespace kv8 {
+
+using namespace sm100;
+using sc::ffma2;
+
+namespace {
+
+constexpr int kPT = 128;            // keys a tile
+constexpr int kPM = 128;            // rows a stage
+constexpr int kPRows = 2 * kPM;     // rows an item
+constexpr int kPThreads = 512;
+constexpr int kGroups = kPT / 16;   // scale groups of a tile
+constexpr int kRing = 4;            // tiles whose scales are kept
+constexpr uint32_t kTmemCols = 512;
+constexpr float kGrow = 8.f;        // log2 of how far P may pass 1
+
+template <int D>
+struct PSmem {
+    uint8_t q[2][kPM * D * 2];    // stages' queries: 64-coordinate blocks of 128 rows x 128 B
+    uint8_t kv[4][kPT * D * 2];   // K of even, odd tiles, V of even, odd tiles
+    uint8_t raw[2][kPT * D];      // codes as they arrive: K, V
+    float kscale[kRing][kGroups], vscale[kRing][kGroups];  // s_k, s_v / R
+    uint32_t absent[kRing];       // 16-key groups without a page
+    float rmax[kRing];            // R of the tile's item
+    float red[4];
+    uint64_t raw_full[2], raw_empty[2], kv_full[4], kv_empty[4];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], mma_done;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// Item of the batch: 256 rows `part` of head `head` of entry `i`.
+struct Item {
+    Entry e;
+    int i, head, part, t0, nt;
+    int64_t per_head;  // tiles of all parts of a head
+};
+
+__device__ __forceinline__ int parts_of(const Attn& a, const Entry& e) {
+    const int64_t rows = (int64_t)e.qn * a.group;
+    return rows > a.few ? (int)((rows + kPRows - 1) / kPRows) : 0;
+}
+// First tile and number of tiles of a part (one at least: rows without keys are
+// written too).
+__device__ __forceinline__ void tiles_of(const Attn& a, const Entry& e, int part, int& t0, int& nt) {
+    const int first = (int)((int64_t)part * kPRows / a.group);
+    const int last = (int)min((int64_t)e.qn - 1, ((int64_t)(part + 1) * kPRows - 1) / a.group);
+    const int end = a.causal ? min(e.len, e.len - e.qn + last + 1) : e.len;
+    const int beg = below_window(a, e.len - e.qn + first) + 1;
+    t0 = beg / kPT;
+    nt = max(1, (end + kPT - 1) / kPT - t0);
+}
+__device__ __forceinline__ int64_t tiles_per_head(const Attn& a, const Entry& e) {
+    int64_t n = 0;
+    for (int p = 0, m = parts_of(a, e); p < m; ++p) {
+        int t0, nt;
+        tiles_of(a, e, p, t0, nt);
+        n += nt;
+    }
+    return n;
+}
+// To step `rem` of entry i's steps; returns the tile within the item.
+__device__ __forceinline__ int open_item(const Attn& a, Item& it, int64_t rem) {
+    it.head = (int)(rem / it.per_head);
+    rem -= it.head * it.per_head;
+    it.part = 0;
+    while (true) {
+        tiles_of(a, it.e, it.part, it.t0, it.nt);
+        if (rem < it.nt) return (int)rem;
+        rem -= it.nt;
+        ++it.part;
+    }
+}
+__device__ __forceinline__ void next_item(const Attn& a, Item& it) {
+    if (++it.part < parts_of(a, it.e)) {
+        tiles_of(a, it.e, it.part, it.t0, it.nt);
+        return;
+    }
+    it.part = 0;
+    if (++it.head == a.v.heads) {
+        it.head = 0;
+        do {
+            it.e = entry_of(a, ++it.i);
+        } while (parts_of(a, it.e) == 0);
+        it.per_head = tiles_per_head(a, it.e);
+    }
+    tiles_of(a, it.e, it.part, it.t0, it.nt);
+}
+
+// A CTA's share of the steps, walked item by item.  Every role walks it alone.
+struct Walk {
+    Item it;
+    int t, t_end;      // tiles of the item that are this CTA's
+    int64_t g, g1;
+    __device__ __forceinline__ bool done() const { return g >= g1; }
+    __device__ __forceinline__ void clip() { t_end = (int)min((int64_t)it.nt, t + (g1 - g)); }
+    __device__ __forceinline__ void next(const Attn& a) {
+        g += t_end - t;
+        if (g >= g1) return;
+        next_item(a, it);
+        t = 0;
+        clip();
+    }
+};
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int FMT, int D, typename T>
+__global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
+                                                              const __grid_constant__ CUtensorMap kmap,
+                                                              const __grid_constant__ CUtensorMap vmap,
+                                                              const PromptParts parts) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    PSmem<D>& sm = *reinterpret_cast<PSmem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+    constexpr int CH = D / 16;   // 16-code chunks of a row
+    constexpr uint32_t kBlock = kPM * 128;  // bytes of such a block
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort = &sm.abort;
+    const int unit = blockIdx.x;
+
+    // ---- the batch's steps: a run of entries a thread, prefix over the block
+    int64_t* pre = reinterpret_cast<int64_t*>(sm.kv);  // (before the operands are)
+    const int run = (a.ns + kPThreads - 1) / kPThreads;
+    {
+        int64_t mine = 0;
+        for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i)
+            mine += a.v.heads * tiles_per_head(a, entry_of(a, i));
+        if (threadIdx.x == 0) {
+            sm.abort = 0;
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sm.raw_full[i], 1);
+                mbar_init(&sm.raw_empty[i], 4);
+                mbar_init(&sm.q_full[i], 4);
+                mbar_init(&sm.s_full[i], 1);
+                mbar_init(&sm.p_full[i], 4);
+                mbar_init(&sm.o_full[i], 1);
+            }
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&sm.kv_full[i], 4);
+                mbar_init(&sm.kv_empty[i], 1);
+            }
+            mbar_init(&sm.mma_done, 1);
+            fence_mbar_init();
+        }
+        int64_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        pre[threadIdx.x + 1] = inc;
+        __syncthreads();
+        int64_t before = 0;
+        for (int w = 0; w < warp; ++w) before += pre[32 * w + 32];
+        __syncthreads();
+        pre[threadIdx.x + 1] = inc + before;
+        if (threadIdx.x == 0) {
+            pre[0] = 0;
+            parts.cut[unit].parts = 0;
+        }
+        __syncthreads();
+    }
+    const int64_t total = pre[kPThreads];
+    const int64_t units = min((int64_t)gridDim.x, total);
+    Walk w = {};
+    if (unit < units) {
+        w.g = unit * total / units;
+        w.g1 = (unit + 1) * total / units;
+        int lo = 0, hi = kPThreads;  // the run of entries that holds step g
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= w.g) lo = mid;
+            else hi = mid;
+        }
+        int64_t rem = w.g - pre[lo];
+        int i = lo * run;
+        while (true) {
+            w.it.e = entry_of(a, i);
+            w.it.per_head = tiles_per_head(a, w.it.e);
+            if (rem < w.it.per_head * a.v.heads) break;
+            rem -= w.it.per_head * a.v.heads;
+            ++i;
+        }
+        w.it.i = i;
+        w.t = open_item(a, w.it, rem);
+        w.clip();
+    }
+    if (warp == 12) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();  // also: nobody reads `pre` any more
+    tc_fence_after();
+    const uint32_t tbase = sm.tmem_base;
+
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = mbar_wait(bar, parity, abort, kWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+            *abort = 1;
+            return false;
+        }
+        return true;
+    };
+
+    if (warp < 8) {
+        // ================================================== softmax, a row a thread
+        regs_up<192>();
+        const int st = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_col = lane_addr + st * kPT, o_col = lane_addr + 2 * kPT + st * D;
+        uint32_t tile = 0, n_s = 0, n_o = 0;  // tiles so far; waits on s_full, o_full
+        bool ok = true;
+        for (; !w.done() && ok; w.next(a)) {
+            const Item& it = w.it;
+            const Entry& e = it.e;
+            const int64_t rows = (int64_t)e.qn * a.group;
+            const int64_t ri = (int64_t)it.part * kPRows + st * kPM + row;
+            if ((int64_t)it.part * kPRows + st * kPM >= rows) {  // the item has one stage
+                tile += w.t_end - w.t;
+                continue;
+            }
+            const bool valid = ri < rows;
+            const int tq = valid ? (int)(ri / a.group) : 0;
+            const int hq = it.head * a.group + (valid ? (int)(ri - (int64_t)tq * a.group) : 0);
+            // ---- the query row, as halves
+            float sl;
+            {
+                const T* q = (const T*)a.q + (e.c0 + tq) * a.q_ts + (int64_t)hq * a.q_hs;
+                Pack<T, 8> x[D / 8];
+                float top = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    if (valid) {
+                        x[c] = *reinterpret_cast<const Pack<T, 8>*>(q + 8 * c);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) from_f(0.f, x[c].v[k]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(to_f(x[c].v[k])));
+                }
+                // (a negative scale turns the row's sign, so that the factor of S is >= 0)
+                const float unit_q = row_unit(top);
+                const float f = a.scale_log2 < 0.f ? -unit_q : unit_q;
+                sl = fabsf(a.scale_log2) / unit_q;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 o;
+                    o.x = half2_bits(to_f(x[c].v[0]) * f, to_f(x[c].v[1]) * f);
+                    o.y = half2_bits(to_f(x[c].v[2]) * f, to_f(x[c].v[3]) * f);
+                    o.z = half2_bits(to_f(x[c].v[4]) * f, to_f(x[c].v[5]) * f);
+                    o.w = half2_bits(to_f(x[c].v[6]) * f, to_f(x[c].v[7]) * f);
+                    *reinterpret_cast<uint4*>(sm.q[st] + (c >> 3) * kBlock + row * 128 +
+                                              (((c & 7) ^ (row & 7)) << 4)) = o;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_full[st]);
+            }
+            const int pos = e.len - e.qn + tq;
+            const int lim = !valid ? e.len - 1 : a.causal ? min(pos, e.len - 1) : e.len - 1;
+            const int low = valid ? below_window(a, pos) : -1;
+            float m = -INFINITY, R = 0.f;
+            float2 L2 = make_float2(0.f, 0.f);
+            for (int t = w.t; t < w.t_end; ++t, ++tile) {
+                const int key0 = (it.t0 + t) * kPT;
+                const int rg = tile & (kRing - 1);
+                if (!wait(&sm.s_full[st], n_s & 1)) {
+                    ok = false;
+                    break;
+                }
+                ++n_s;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, s[c]);
+                float cg[kGroups];
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) cg[g] = sl * sm.kscale[rg][g];
+                const uint32_t absent = sm.absent[rg];
+                if (t == w.t) R = sm.rmax[rg];
+                tmem_wait_ld();
+                if (__any_sync(0xffffffffu, key0 + kPT - 1 > lim || key0 <= low || absent)) {
+#pragma unroll
+                    for (int i = 0; i < kPT; ++i) {
+                        const int key = key0 + i;
+                        const bool see = key <= lim && key > low && !(absent >> (i / 16) & 1u);
+                        s[i / 32][i % 32] = see ? __float_as_uint(__uint_as_float(s[i / 32][i % 32]) * cg[i / 16])
+                                                : 0xff800000u;
+                    }
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) cg[g] = 1.f;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    float x = __uint_as_float(s[g / 2][(g & 1) * 16]);
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) x = fmaxf(x, __uint_as_float(s[g / 2][(g & 1) * 16 + i]));
+                    top = fmaxf(top, x * cg[g]);
+                }
+                // the reference follows when the maximum has grown past it by kGrow
+                const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
+                float shrink = 1.f;
+                if (grow) {
+                    shrink = ex2(m - top);  // 0 from -infinity
+                    m = top;
+                    L2.x *= shrink;
+                    L2.y *= shrink;
+                }
+                if (t > w.t && __any_sync(0xffffffffu, grow)) {
+                    // S of this tile is complete, so O += P V of the last one is too
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_col + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+                        tmem_st16(o_col + c, o);
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int g = 2 * c + h;
+                        const float vw = sm.vscale[rg][g];
+                        const float2 cc = make_float2(cg[g], cg[g]), bb = make_float2(base, base);
+                        const float2 ww = make_float2(vw, vw);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float2 x = make_float2(__uint_as_float(s[c][16 * h + 2 * i]),
+                                                   __uint_as_float(s[c][16 * h + 2 * i + 1]));
+                            x = ffma2(x, cc, bb);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            L2 = __fadd2_rn(L2, x);
+                            x = __fmul2_rn(x, ww);
+                            p[8 * h + i] = half2_bits(x.x, x.y);
+                        }
+                    }
+                    tmem_st16(s_col + 16 * c, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[st]);
+            }
+            if (!ok) break;
+            if (!wait(&sm.o_full[st], n_o & 1)) {
+                ok = false;
+                break;
+            }
+            ++n_o;
+            tc_fence_after();
+            const float L = L2.x + L2.y;
+            const bool begins = w.t == 0, ends = w.t_end == it.nt;
+            if (begins && ends) {
+                const float n = L > 0.f ? R / L : (L == 0.f ? 0.f : L);
+                T* out = (T*)a.out + ((e.c0 + tq) * a.heads_q + hq) * D;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_col + c, o);
+                    tmem_wait_ld();
+                    if (valid) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            Pack<T, 8> y;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) from_f(__uint_as_float(o[8 * h + k]) * n, y.v[k]);
+                            *reinterpret_cast<Pack<T, 8>*>(out + c + 8 * h) = y;
+                        }
+                    }
+                }
+                if (a.lse && valid)
+                    a.lse[(e.c0 + tq) * a.heads_q + hq] = L > 0.f ? (m + log2f(L)) * 0.69314718056f : (L == 0.f ? -INFINITY : L);
+            } else {
+                const int64_t slot = 2 * (int64_t)unit + (begins ? 1 : 0);
+                const int64_t pr = slot * kPRows + st * kPM + row;
+                if (valid) parts.ml[pr] = make_float2(m, L);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_col + c, o);
+                    tmem_wait_ld();
+                    if (valid) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<float4*>(parts.o + pr * D + c + k) =
+                                make_float4(__uint_as_float(o[k]) * R, __uint_as_float(o[k + 1]) * R,
+                                            __uint_as_float(o[k + 2]) * R, __uint_as_float(o[k + 3]) * R);
+                    }
+                }
+                if (begins && st == 0 && row == 0) {
+                    const int64_t last = w.g + it.nt - 1;  // the item's last step: its CTA
+                    Cut c;
+                    c.parts = (int)(((last + 1) * units - 1) / total) - unit + 1;
+                    c.rows = (int)min((int64_t)kPRows, rows - (int64_t)it.part * kPRows);
+                    c.head = it.head;
+                    c.pad = 0;
+                    c.row0 = e.c0 * a.group + (int64_t)it.part * kPRows;
+                    parts.cut[unit] = c;
+                }
+            }
+            tc_fence_before();  // O is read before the next item's MMAs write it
+        }
+    } else {
+        regs_down<64>();
+        if (warp < 12) {
+            // ============================================== codes -> halves
+            const int tid = threadIdx.x - 256;
+            uint32_t tile = 0, n_raw = 0;
+            bool ok = true;
+            for (; !w.done() && ok; w.next(a)) {
+                const Item& it = w.it;
+                const Entry& e = it.e;
+                // R: the largest value scale of the keys of this CTA's part
+                const int k0 = (it.t0 + w.t) * kPT, k1 = min(e.len, (it.t0 + w.t_end) * kPT);
+                float R = 0.f;
+                for (int p = (k0 >> a.v.page_log2) + tid; p <= (k1 - 1) >> a.v.page_log2 && k1 > k0; p += 128) {
+                    const int pid = page_of(a.v, e.slot, p);
+                    if (pid >= 0) R = fmaxf(R, __ldg(a.vs + (int64_t)pid * a.v.heads + it.head));
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
+                if (lane == 0) sm.red[warp - 8] = R;
+                named_bar(1, 128);
+                R = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
+                named_bar(1, 128);
+                // (scales below fp32's normal range have no reciprocal: their values count as 0)
+                const float inv = R >= 1.17549435e-38f ? 1.f / R : 0.f;
+                // thread g < 8: s_k of the next tile's 16-key group g; 8..15: s_v; NaN: no page
+                auto load_scale = [&](int t) {
+                    float x = 0.f;
+                    if (tid < 16) {
+                        const int key = (it.t0 + t) * kPT + 16 * (tid & 7);
+                        const int pid = key < e.len ? page_of(a.v, e.slot, key >> a.v.page_log2) : -1;
+                        if (pid >= 0) x = __ldg((tid < 8 ? a.ks : a.vs) + (int64_t)pid * a.v.heads + it.head);
+                        else x = tid < 8 ? -1.f : 0.f;
+                    }
+                    return x;
+                };
+                float next = load_scale(w.t);
+                for (int t = w.t; t < w.t_end && ok; ++t, ++tile) {
+                    const int key0 = (it.t0 + t) * kPT;
+                    const float sc = next;
+                    if (t + 1 < w.t_end) next = load_scale(t + 1);
+#pragma unroll 1
+                    for (int isv = 0; isv < 2; ++isv) {
+                        const int slot = 2 * isv + (tile & 1);
+                        const uint32_t b = n_raw & 1, ph = (n_raw >> 1) & 1;
+                        if (!wait(&sm.raw_full[b], ph) ||
+                            (tile >= 2 && !wait(&sm.kv_empty[slot], ((tile >> 1) - 1) & 1))) {
+                            ok = false;
+                            break;
+                        }
+                        ++n_raw;
+                        if (isv == 0 && warp == 8) {
+                            const int rg = tile & (kRing - 1);
+                            const uint32_t gone = __ballot_sync(0xffffffffu, tid < 8 && sc < 0.f);
+                            if (tid < 8) sm.kscale[rg][tid] = fmaxf(sc, 0.f);
+                            else if (tid < 16) sm.vscale[rg][tid - 8] = sc * inv;
+                            if (tid == 0) {
+                                sm.absent[rg] = gone;
+                                sm.rmax[rg] = R;
+                            }
+                        }
+                        const uint8_t* src = sm.raw[b];
+                        uint8_t* dst = sm.kv[slot];
+#pragma unroll 4
+                        for (int i = 0; i < CH; ++i) {
+                            const int idx = tid + 128 * i, r = idx / CH, c = idx % CH;
+                            const uint32_t off = D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4))
+                                                          : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                            uint4 x = *reinterpret_cast<const uint4*>(src + off);
+                            uint4 y0, y1;
+                            // rows behind the slot's end: 0 (e4m3 rubbish may be NaN)
+                            if (FMT == TQ_KV_E4M3 && key0 + r >= e.len) x = make_uint4(0, 0, 0, 0);
+                            codes_to_half<FMT>(x.x, y0.x, y0.y);
+                            codes_to_half<FMT>(x.y, y0.z, y0.w);
+                            codes_to_half<FMT>(x.z, y1.x, y1.y);
+                            codes_to_half<FMT>(x.w, y1.z, y1.w);
+                            uint8_t* d = dst + (c >> 2) * kBlock + r * 128;
+                            const int c0 = (c & 3) * 2;
+                            uint4* p0 = reinterpret_cast<uint4*>(d + ((c0 ^ (r & 7)) << 4));
+                            uint4* p1 = reinterpret_cast<uint4*>(d + (((c0 + 1) ^ (r & 7)) << 4));
+                            // the second block's lanes write in the other order: no bank twice
+                            const bool swap = c >= 4;
+                            *(swap ? p1 : p0) = swap ? y1 : y0;
+                            *(swap ? p0 : p1) = swap ? y0 : y1;
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sm.kv_full[slot]);
+                            mbar_arrive(&sm.raw_empty[b]);
+                        }
+                    }
+                }
+            }
+        } else if (warp == 12) {
+            // ============================================== MMAs
+            constexpr uint32_t kQK = idesc_f16(0, kPM, kPT);
+            constexpr uint32_t kPV = idesc_f16(0, kPM, D) | (1u << 16);  // B MN-major
+            const uint32_t qb = smem_u32(sm.q[0]), kvb = smem_u32(sm.kv[0]);
+            constexpr uint32_t kQBytes = kPM * D * 2;
+            uint32_t tile = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+            bool ok = true;
+            auto qk = [&](int st, uint32_t u) {  // S of tile u
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = (k >> 2) * kBlock + (k & 3) * 32;
+                        mma_f16_ss(tbase + st * kPT, smem_desc_kmajor_sw128(qb + st * kQBytes + off),
+                                   smem_desc_kmajor_sw128(kvb + (u & 1) * kQBytes + off), kQK, k > 0);
+                    }
+                    tc_commit(&sm.s_full[st]);
+                }
+            };
+            auto pv = [&](int st, uint32_t u, bool first) {
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < kPT / 16; ++k)
+                        mma_f16_ts(tbase + 2 * kPT + st * D, tbase + st * kPT + 8 * k,
+                                   smem_desc_mnmajor_sw128(kvb + (2 + (u & 1)) * kQBytes + k * 2048, kBlock),
+                                   kPV, !(first && k == 0));
+                }
+            };
+            for (; !w.done() && ok; w.next(a)) {
+                const int64_t rows = (int64_t)w.it.e.qn * a.group - (int64_t)w.it.part * kPRows;
+                const int nst = rows > kPM ? 2 : 1;
+                for (int st = 0; st < nst && ok; ++st) {
+                    ok = wait(&sm.q_full[st], n_q[st] & 1);
+                    ++n_q[st];
+                }
+                if (ok) ok = wait(&sm.kv_full[tile & 1], (tile >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int st = 0; st < nst; ++st) qk(st, tile);
+                if (lane == 0) tc_commit(&sm.kv_empty[tile & 1]);
+                for (int t = w.t; t < w.t_end && ok; ++t, ++tile) {
+                    const bool more = t + 1 < w.t_end;
+                    if (more) ok = wait(&sm.kv_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
+                    if (ok) ok = wait(&sm.kv_full[2 + (tile & 1)], (tile >> 1) & 1);
+                    for (int st = 0; st < nst && ok; ++st) {
+                        ok = wait(&sm.p_full[st], n_p[st] & 1);
+                        ++n_p[st];
+                        if (!ok) break;
+                        tc_fence_after();
+                        pv(st, tile, t == w.t);
+                        if (more) qk(st, tile + 1);
+                        else if (lane == 0) tc_commit(&sm.o_full[st]);
+                    }
+                    if (ok && lane == 0) {
+                        tc_commit(&sm.kv_empty[2 + (tile & 1)]);
+                        if (more) tc_commit(&sm.kv_empty[(tile + 1) & 1]);
+                    }
+                }
+            }
+            // all MMAs are done before tensor and shared memory go
+            if (lane == 0) {
+                tc_commit(&sm.mma_done);
+                int none = 0;
+                mbar_wait(&sm.mma_done, 0, &none, kWaitNs);
+            }
+            __syncwarp();
+        } else if (warp == 13) {
+            // ============================================== TMA
+            const int box = a.v.page, nbox = kPT / box;
+            uint32_t n = 0;
+            bool ok = true;
+            for (; !w.done() && ok; w.next(a)) {
+                const Item& it = w.it;
+                for (int t = w.t; t < w.t_end && ok; ++t) {
+                    const int key = (it.t0 + t) * kPT + lane * box;
+                    int row = a.rows;  // behind the tensor: zeros
+                    if (lane < nbox && key < it.e.len) {
+                        const int pid = page_of(a.v, it.e.slot, key >> a.v.page_log2);
+                        if (pid >= 0) row = (int)(((int64_t)pid * a.v.heads + it.head) << a.v.page_log2);
+                    }
+                    for (int isv = 0; isv < 2; ++isv, ++n) {
+                        const uint32_t b = n & 1;
+                        if (n >= 2 && !wait(&sm.raw_empty[b], ((n >> 1) - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[b], kPT * D);
+                        __syncwarp();
+                        if (lane < nbox)
+                            tma_load_2d(sm.raw[b] + lane * box * D, isv ? &vmap : &kmap, 0, row, &sm.raw_full[b]);
+                    }
+                }
+            }
+            if (!ok) {  // no copy may land after the block has gone
+                int none = 0;
+                for (uint32_t i = n >= 2 ? n - 2 : 0; i < n; ++i)
+                    mbar_wait(&sm.raw_full[i & 1], (i >> 1) & 1, &none, kWaitNs);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_dealloc(tbase, kTmemCols);
+    if (threadIdx.x == 0) parts.block_status[unit] = sm.abort ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 81 : 0;
+}
+
+// Joins the parts of the items that were cut: blocks (u, y) the item that begins
+// in CTA u, a warp a row, 4 coordinates a lane (d = 128) or 2.
+template <int D, typename T>
+__global__ __launch_bounds__(256) void k_prompt_merge(const Attn a, const PromptParts parts, int blocks) {
+    const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (u == 0 && blockIdx.y == 0) {
+        int st = 0;
+        for (int i = threadIdx.x; i < blocks; i += 256) st |= parts.block_status[i] != 0;
+        st = __syncthreads_or(st);
+        // (the few-rows kernel of the call has set the word; a time-out stands)
+        if (threadIdx.x == 0 && (st || !parts.keep_status)) *parts.status = st ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 81 : 0;
+    }
+    const Cut c = parts.cut[u];
+    if (c.parts == 0) return;
+    constexpr int E = D / 32;
+    auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)u + 1 : 2 * (int64_t)(u + i); };
+    for (int r = blockIdx.y * 8 + warp; r < c.rows; r += gridDim.y * 8) {
+        float m = -INFINITY;
+        for (int i = lane; i < c.parts; i += 32) m = fmaxf(m, parts.ml[slot(i) * kPRows + r].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        float L = 0.f, acc[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) acc[k] = 0.f;
+#pragma unroll 2
+        for (int i = 0; i < c.parts; ++i) {
+            const int64_t pr = slot(i) * kPRows + r;
+            const float2 ml = parts.ml[pr];
+            const float f = ex2(ml.x - base);
+            L = fmaf(f, ml.y, L);
+            const float* src = parts.o + pr * D + lane * E;
+            float x[E];
+            if (E == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+            else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+            for (int k = 0; k < E; ++k) acc[k] = fmaf(f, x[k], acc[k]);
+        }
+        const int64_t ri = c.row0 + r, tok = ri / a.group;
+        const int hq = c.head * a.group + (int)(ri - tok * a.group);
+        const float n = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+        T* out = (T*)a.out + (tok * a.heads_q + hq) * D + lane * E;
+        Pack<T, E> y;
+#pragma unroll
+        for (int k = 0; k < E; ++k) from_f(acc[k] * n, y.v[k]);
+        *reinterpret_cast<Pack<T, E>*>(out) = y;
+        if (a.lse && lane == 0)
+            a.lse[tok * a.heads_q + hq] = L > 0.f ? (m + log2f(L)) * 0.69314718056f : (L == 0.f ? -INFINITY : L);
+    }
+}
+
+template <int FMT, int D, typename T>
+int go(const Attn& a, const CUtensorMap& km, const CUtensorMap& vm, const PromptParts& p, int blocks,
+       cudaStream_t s) {
+    auto kern = k_attn_prompt<FMT, D, T>;
+    constexpr int smem = (int)sizeof(PSmem<D>) + 1024;
+    static_assert(smem <= 232448, "shared memory of a block");
+    TQ_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    kern<<<blocks, kPThreads, smem, s>>>(a, km, vm, p);
+    TQ_CHECK_LAUNCH();
+    k_prompt_merge<D, T><<<dim3((unsigned)blocks, 16), 256, 0, s>>>(a, p, blocks);
+    TQ_CHECK_LAUNCH();
+    return TQ_OK;
+}
+
+template <int D>
+int go_d(const tq_kv8_t* c, const Attn& a, const CUtensorMap& km, const CUtensorMap& vm,
+         const PromptParts& p, int blocks, int q_dtype, cudaStream_t s) {
+    if (c->format == TQ_KV_I8)
+        return q_dtype == TQ_BF16 ? go<TQ_KV_I8, D, __nv_bfloat16>(a, km, vm, p, blocks, s)
+                                  : go<TQ_KV_I8, D, __half>(a, km, vm, p, blocks, s);
+    return q_dtype == TQ_BF16 ? go<TQ_KV_E4M3, D, __nv_bfloat16>(a, km, vm, p, blocks, s)
+                              : go<TQ_KV_E4M3, D, __half>(a, km, vm, p, blocks, s);
+}
+
+}  // namespace
+
+int prompt_blocks(const tq_kv8_t* c, int ns, int64_t total_q, int heads_q) {
+    const int64_t tiles = ((int64_t)c->max_pages * c->page + kPT - 1) / kPT;
+    const int64_t most = tiles * (total_q * (heads_q / c->heads) / kPRows + ns) * c->heads;
+    return (int)(most < 148 ? (most < 1 ? 1 : most) : 148);
+}
+
+PromptParts prompt_carve(const tq_kv8_t* c, void* ws, int blocks, size_t* bytes) {
+    PromptParts p;
+    char* at = (char*)ws;
+    p.status = nullptr;
+    p.keep_status = 0;
+    p.block_status = (int*)at;
+    at += align256(blocks * 4);
+    p.cut = (Cut*)at;
+    at += align256(blocks * sizeof(Cut));
+    p.ml = (float2*)at;
+    at += align256((size_t)2 * blocks * kPRows * sizeof(float2));
+    p.o = (float*)at;
+    at += align256((size_t)2 * blocks * kPRows * c->d * 4);
+    *bytes = (size_t)(at - (char*)ws);
+    return p;
+}
+
+int launch_prompt(const tq_kv8_t* c, int layer, const Attn& a, const PromptParts& p, int blocks,
+                  int q_dtype, cudaStream_t s) {
+    CUtensorMap km, vm;
+    int rc = code_map(&km, (const char*)c->d_k + layer * layer_bytes(c), c->d, a.rows, c->page);
+    if (!rc) rc = code_map(&vm, (const char*)c->d_v + layer * layer_bytes(c), c->d, a.rows, c->page);
+    if (rc) return rc;
+    return c->d == 128 ? go_d<128>(c, a, km, vm, p, blocks, q_dtype, s)
+                       : go_d<64>(c, a, km, vm, p, blocks, q_dtype, s);
+}
+
+}  // namespace kv8
+}  // namespace tq

@@ -221,10 +221,10 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor_sw128(uint32_t saddr) {
 // canonical layout: rows of 64 16-bit elements (128 B) along M/N, one row per
 // K index, 8-row atoms 1024 bytes apart (stride byte offset); the leading
 // byte offset steps between 64-element M/N blocks (unused for N = 64).
-__device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t saddr) {
+__device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t saddr, uint32_t lbo = 8192u) {
     uint64_t desc = 0;
     desc |= (uint64_t)((saddr >> 4) & 0x3FFFu);        // start address
-    desc |= (uint64_t)(8192u >> 4) << 16;                // leading byte offset
+    desc |= (uint64_t)(lbo >> 4) << 16;                  // leading byte offset
     desc |= (uint64_t)(1024u >> 4) << 32;                // stride byte offset: 8 K-rows
     desc |= (uint64_t)1u << 46;                          // descriptor version (sm100)
     desc |= (uint64_t)2u << 61;                          // layout: 128-byte swizzle

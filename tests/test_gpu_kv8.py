@@ -514,6 +514,42 @@ def test_attention_repeats_bit_for_bit(tq_lib, cuda, counts):
         assert torch.equal(first, c.attention(0, q, cu_of(counts, cuda), max(counts)))
 
 
+@pytest.mark.parametrize("counts", [[2], [1, 3], [0, 7]])
+def test_attention_padded_batch(tq_lib, cuda, counts):
+    """q may be longer than the batch, and max_q larger than any count: every
+    token of the batch is computed, what lies behind stays."""
+    lens = [90, 300][:len(counts)]
+    c = fill(tq_lib, cuda, "i8", 2, 64, 32, lens)
+    total, used = 100 * len(counts), sum(counts)
+    q = torch.randn(total, 8, 64, generator=gen(3)).to(torch.bfloat16).to(cuda)
+    want = check_attention(c, q[:used], counts, lens)
+    for max_q in (max(counts), 50, 100, 200):
+        out = torch.full_like(q, 3.0)
+        c.attention(0, q, cu_of(counts, cuda), max_q, out=out)
+        c.status()
+        at = 0
+        for i, (m, n) in enumerate(zip(counts, lens)):
+            k, v = values(c, "k", 0, i, n), values(c, "v", 0, i, n)
+            ref, bound, _ = dense(q[at:at + m].cpu(), k, v, visible(m, n, True, 0), 64 ** -0.5)
+            assert_near(out[at:at + m], ref, bound)
+            at += m
+        assert (out[used:] == 3.0).all()
+        assert want.shape[0] == used
+
+
+@pytest.mark.parametrize("counts", [[5, 1], [90, 70]])
+def test_attention_widest_window(tq_lib, cuda, counts):
+    """Windows beyond every length, up to the largest int, hide nothing; more
+    queries than tokens among them."""
+    lens = [3, 200]
+    c = fill(tq_lib, cuda, "i8", 2, 128, 64, lens)
+    q = torch.randn(sum(counts), 4, 128, generator=gen(3)).to(torch.bfloat16).to(cuda)
+    want = check_attention(c, q, counts, lens)
+    for window in (1 << 20, 2 ** 31 - 1):
+        got = c.attention(0, q, cu_of(counts, cuda), max(counts), window=window)
+        assert torch.equal(got, want)
+
+
 # ------------------------------------------------------------------ pages
 
 class Model:
