@@ -1,4 +1,5 @@
-"""Build libtq.so (the sm_100a CUDA library behind include/tq.h) in-tree."""
+"""Build libtq.so (the sm_100a CUDA library behind include/tq.h) and _kv8.so (the
+torch side of its paged-cache calls) in-tree."""
 import glob
 import os
 import subprocess
@@ -9,6 +10,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtq.so")
+BIND_SRC = os.path.join(CSRC, "kv8_bind.cpp")
+BIND = os.path.join(PKG, "_kv8.so")
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
@@ -23,11 +26,28 @@ def sources():
 
 
 def _stale():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "tq.h")]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    deps = [BIND_SRC] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "tq.h")]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _bind_command(out):
+    """g++ over kv8_bind.cpp against this interpreter's torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [INCLUDE, os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{i}" for i in inc), BIND_SRC, "-o", out,
+            f"-L{PKG}", "-l:libtq.so", "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(root, 'lib')}",
+            "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
 def build(force=False, verbose=False):
@@ -54,6 +74,8 @@ def build(force=False, verbose=False):
     cmd = [nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp, *objs]
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+    subprocess.check_call(_bind_command(BIND + ".tmp"))
+    os.replace(BIND + ".tmp", BIND)
     return LIB
 
 

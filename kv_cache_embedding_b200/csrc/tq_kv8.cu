@@ -60,6 +60,7 @@ template <typename T, int FMT, int VEC, int NI>
 __global__ __launch_bounds__(256) void k_append(const AppendArgs a,
                                                 const __grid_constant__ tq_rope_params_t rope) {
     __shared__ float s_red[8];
+    grid_begin();
     const View& v = a.v;
     const int seq = blockIdx.x / a.ppb, pj = blockIdx.x - seq * a.ppb;
     const int h = blockIdx.y, kv = blockIdx.z;
@@ -194,9 +195,8 @@ template <typename T, int FMT, int VEC, int NI>
 int append_go(const AppendArgs& a, const tq_rope_params_t& r, int ns, int threads, cudaStream_t s) {
     const int64_t gx = (int64_t)ns * a.ppb;
     if (gx > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
-    k_append<T, FMT, VEC, NI><<<dim3((unsigned)gx, (unsigned)a.v.heads, 2), threads, 0, s>>>(a, r);
-    TQ_CHECK_LAUNCH();
-    return TQ_OK;
+    return launch_behind(k_append<T, FMT, VEC, NI>, dim3((unsigned)gx, (unsigned)a.v.heads, 2), threads, 0,
+                         s, a, r);
 }
 
 // Threads and items a thread for the most rows that a block can get.
@@ -234,15 +234,16 @@ constexpr int kReadThreads = 256;
 
 // A block reads `tokens` tokens of one slot, all heads, K and V: 16 codes a step.
 template <typename T, int FMT>
-__global__ __launch_bounds__(kReadThreads) void k_read(View v, const int32_t* __restrict__ slots,
-                                                       const int32_t* __restrict__ begin,
-                                                       const int32_t* __restrict__ cu, int bps,
+__global__ __launch_bounds__(kReadThreads) void k_read(View v, const int32_t* slots,
+                                                       const int32_t* begin,
+                                                       const int32_t* cu, int bps,
                                                        int tokens, int64_t total,
-                                                       const uint8_t* __restrict__ kc,
-                                                       const uint8_t* __restrict__ vc,
-                                                       const float* __restrict__ ks,
-                                                       const float* __restrict__ vs, T* out_k,
+                                                       const uint8_t* kc,
+                                                       const uint8_t* vc,
+                                                       const float* ks,
+                                                       const float* vs, T* out_k,
                                                        T* out_v) {
+    grid_begin();
     const int seq = blockIdx.x / bps, blk = blockIdx.x - seq * bps;
     const int slot = slot_of(v, slots, seq);
     const int64_t c0 = max(cu[seq], 0);
@@ -296,14 +297,9 @@ int read_type(const tq_kv8_t* c, int layer, int ns, const int32_t* slots, const 
     const uint8_t* vc = (const uint8_t*)c->d_v + layer * layer_bytes(c);
     const float* ks = c->d_kscale + layer * layer_scales(c);
     const float* vs = c->d_vscale + layer * layer_scales(c);
-    if (c->format == TQ_KV_I8)
-        k_read<T, TQ_KV_I8><<<grid, kReadThreads, 0, s>>>(view(c), slots, begin, cu, (int)bps, tokens,
-                                                          total, kc, vc, ks, vs, (T*)k, (T*)v);
-    else
-        k_read<T, TQ_KV_E4M3><<<grid, kReadThreads, 0, s>>>(view(c), slots, begin, cu, (int)bps,
-                                                            tokens, total, kc, vc, ks, vs, (T*)k, (T*)v);
-    TQ_CHECK_LAUNCH();
-    return TQ_OK;
+    return launch_behind(c->format == TQ_KV_I8 ? k_read<T, TQ_KV_I8> : k_read<T, TQ_KV_E4M3>, grid,
+                         kReadThreads, 0, s, view(c), slots, begin, cu, (int)bps, tokens, total, kc, vc,
+                         ks, vs, (T*)k, (T*)v);
 }
 
 }  // namespace

@@ -4,6 +4,7 @@
 #include <cuda_fp8.h>
 
 #include "tq_internal.cuh"
+#include "tq_launch.cuh"
 
 namespace tq {
 namespace kv8 {

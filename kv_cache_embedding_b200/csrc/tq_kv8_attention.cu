@@ -163,6 +163,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     const int64_t umax = (int64_t)gridDim.x * kWarps;
     WarpSmem<D>& ws = sm.w[warp];
     volatile int* abort = &sm.abort;
+    grid_begin();
 
     // ---- the batch's steps: a run of entries a thread, prefix over the block
     const int run = (a.ns + kThreads - 1) / kThreads;
@@ -247,7 +248,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                 uint8_t* dst = (isv ? ws.v[pstage] : ws.k[pstage]) + hf * box * D;
                 tma_load_2d(dst, isv ? &vmap : &kmap, 0, row, bar);
             }
-            pend = pid < 0 ? (isv ? 0.f : -INFINITY) : __ldg((isv ? a.vs : a.ks) + ph);
+            pend = pid < 0 ? (isv ? 0.f : -INFINITY) : (isv ? a.vs : a.ks)[ph];
         }
         pend_stage = pstage;
         pstage = pstage + 1 == kStages ? 0 : pstage + 1;
@@ -522,6 +523,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
 template <int D, typename T>
 __global__ __launch_bounds__(128) void k_attn_merge(const Attn a, const Parts parts, int blocks) {
     const int u = blockIdx.x, r = blockIdx.y;
+    grid_begin();
     if (u == 0 && r == 0) {  // the call's status
         int st = 0;
         for (int i = threadIdx.x; i < blocks; i += 128) st = min(st, parts.block_status[i]);
@@ -620,14 +622,12 @@ Parts carve(void* ws, int64_t blocks, size_t* bytes) {
 template <int FMT, int D, typename T>
 int launch(const Attn& a, const CUtensorMap& km, const CUtensorMap& vm, const Parts& p, int blocks,
            int cuts, int rows, cudaStream_t s) {
-    auto kern = k_attn_rows<FMT, D, T>;
     constexpr int smem = (int)sizeof(Smem<D>) + 1024;
-    TQ_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    kern<<<blocks, kThreads, smem, s>>>(a, km, vm, p);
-    TQ_CHECK_LAUNCH();
-    k_attn_merge<D, T><<<dim3((unsigned)cuts, (unsigned)rows), 128, 0, s>>>(a, p, blocks);
-    TQ_CHECK_LAUNCH();
-    return TQ_OK;
+    int rc = allow_smem<k_attn_rows<FMT, D, T>>(smem);
+    if (!rc) rc = launch_behind(k_attn_rows<FMT, D, T>, dim3(blocks), kThreads, smem, s, a, km, vm, p);
+    if (!rc)
+        rc = launch_behind(k_attn_merge<D, T>, dim3((unsigned)cuts, (unsigned)rows), 128, 0, s, a, p, blocks);
+    return rc;
 }
 
 template <int D>

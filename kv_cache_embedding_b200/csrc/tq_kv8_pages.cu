@@ -98,11 +98,12 @@ __device__ __forceinline__ bool repeated(const View& v, const int32_t* slots, in
 
 __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t* len,
                                                  int32_t* refs, int n,
-                                                 const int32_t* __restrict__ slots,
-                                                 const int32_t* __restrict__ counts, PagesWs w) {
+                                                 const int32_t* slots,
+                                                 const int32_t* counts, PagesWs w) {
     __shared__ int64_t tmp[33];
     __shared__ int32_t s_held[kMaxList];  // the shared page that entry i writes into, or -1
     __shared__ int32_t s_base[kMaxList];  // first of the entry's new pages
+    grid_begin();
     bool bad = repeated(v, slots, n, w.marks);
     if (threadIdx.x == 0) w.head[1] = 0;
     int at[kPer], more[kPer], need[kPer];
@@ -223,8 +224,9 @@ __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t
 }
 
 __global__ __launch_bounds__(kPT) void k_fork(View v, int32_t* table, int32_t* len, int32_t* refs,
-                                              int n, const int32_t* __restrict__ parents,
-                                              const int32_t* __restrict__ children, PagesWs w) {
+                                              int n, const int32_t* parents,
+                                              const int32_t* children, PagesWs w) {
+    grid_begin();
     // marks: parents cleared first, then the children counted
     for (int i = threadIdx.x; i < n; i += kPT)
         if ((unsigned)parents[i] < (unsigned)v.slots) w.marks[parents[i]] = 0;
@@ -253,8 +255,9 @@ __global__ __launch_bounds__(kPT) void k_fork(View v, int32_t* table, int32_t* l
 
 __global__ __launch_bounds__(kPT) void k_truncate(View v, int32_t* table, int32_t* len,
                                                   int32_t* refs, int n,
-                                                  const int32_t* __restrict__ slots,
-                                                  const int32_t* __restrict__ lens, PagesWs w) {
+                                                  const int32_t* slots,
+                                                  const int32_t* lens, PagesWs w) {
+    grid_begin();
     bool bad = repeated(v, slots, n, w.marks);
     for (int i = threadIdx.x; i < n; i += kPT)
         bad |= (unsigned)slots[i] >= (unsigned)v.slots || lens[i] < 0;
@@ -279,6 +282,7 @@ __global__ __launch_bounds__(kPT) void k_truncate(View v, int32_t* table, int32_
 // its movers and holes.
 __global__ __launch_bounds__(kPT) void k_compact(View v, int32_t* refs, PagesWs w) {
     __shared__ int64_t tmp[33];
+    grid_begin();
     const int64_t run = ((int64_t)v.pages + kPT - 1) / kPT;
     const int64_t p0 = min((int64_t)v.pages, threadIdx.x * run), p1 = min((int64_t)v.pages, p0 + run);
     int64_t live = 0, L, moves;
@@ -318,13 +322,14 @@ __global__ __launch_bounds__(kPT) void k_compact(View v, int32_t* refs, PagesWs 
 constexpr int kCT = 256, kPiece = kCT * 16 * 4;
 
 template <bool REMAP>
-__global__ __launch_bounds__(kCT) void k_copy_pages(const int* __restrict__ head,
-                                                    const int32_t* __restrict__ src,
-                                                    const int32_t* __restrict__ dst,
-                                                    const int32_t* __restrict__ remap, int layers,
+__global__ __launch_bounds__(kCT) void k_copy_pages(const int* head,
+                                                    const int32_t* src,
+                                                    const int32_t* dst,
+                                                    const int32_t* remap, int layers,
                                                     int pages, int heads, int64_t page_bytes,
                                                     uint8_t* k, uint8_t* v, float* ks, float* vs,
                                                     int32_t* table, int64_t entries) {
+    grid_begin();
     if (head[0] != TQ_OK) return;
     const int pairs = head[1];
     const int64_t pieces = (page_bytes + kPiece - 1) / kPiece;
@@ -370,11 +375,9 @@ int copy_pages(const tq_kv8_t* c, const PagesWs& w, int64_t most, cudaStream_t s
     int64_t blocks = most * c->layers * 2 * pieces;
     if (blocks < (entries + kCT - 1) / kCT) blocks = (entries + kCT - 1) / kCT;
     if (blocks > 148 * 8) blocks = 148 * 8;
-    k_copy_pages<REMAP><<<(unsigned)blocks, kCT, 0, s>>>(
-        w.head, w.src, w.dst, w.ids, c->layers, c->pages, c->heads, page_bytes, (uint8_t*)c->d_k,
-        (uint8_t*)c->d_v, c->d_kscale, c->d_vscale, c->d_table, entries);
-    TQ_CHECK_LAUNCH();
-    return TQ_OK;
+    return launch_behind(k_copy_pages<REMAP>, dim3((unsigned)blocks), kCT, 0, s, w.head, w.src, w.dst, w.ids,
+                         c->layers, c->pages, c->heads, page_bytes, (uint8_t*)c->d_k, (uint8_t*)c->d_v,
+                         c->d_kscale, c->d_vscale, c->d_table, entries);
 }
 
 // The checks that the list operations share.
@@ -397,45 +400,37 @@ using namespace tq;
 
 extern "C" int tq_kv8_reserve(const tq_kv8_t* c, int n, const int32_t* d_slots,
                               const int32_t* d_counts, void* d_ws, size_t ws_bytes, void* stream) {
-    const int rc = kv8::check_list(c, n, d_slots, d_counts, d_ws, ws_bytes);
+    int rc = kv8::check_list(c, n, d_slots, d_counts, d_ws, ws_bytes);
     if (rc || n == 0) return rc;
     const kv8::PagesWs w = kv8::carve(c, n, d_ws);
     cudaStream_t s = (cudaStream_t)stream;
-    kv8::k_reserve<<<1, kv8::kPT, 0, s>>>(kv8::view(c), c->d_table, c->d_len, c->d_refs, n, d_slots,
-                                          d_counts, w);
-    TQ_CHECK_LAUNCH();
-    return kv8::copy_pages<false>(c, w, n, s);
+    rc = launch_behind(kv8::k_reserve, dim3(1), kv8::kPT, 0, s, kv8::view(c), c->d_table, c->d_len,
+                                  c->d_refs, n, d_slots, d_counts, w);
+    return rc ? rc : kv8::copy_pages<false>(c, w, n, s);
 }
 
 extern "C" int tq_kv8_fork(const tq_kv8_t* c, int n, const int32_t* d_parents,
                            const int32_t* d_children, void* d_ws, size_t ws_bytes, void* stream) {
     const int rc = kv8::check_list(c, n, d_parents, d_children, d_ws, ws_bytes);
     if (rc || n == 0) return rc;
-    kv8::k_fork<<<1, kv8::kPT, 0, (cudaStream_t)stream>>>(kv8::view(c), c->d_table, c->d_len,
-                                                          c->d_refs, n, d_parents, d_children,
-                                                          kv8::carve(c, n, d_ws));
-    TQ_CHECK_LAUNCH();
-    return TQ_OK;
+    return launch_behind(kv8::k_fork, dim3(1), kv8::kPT, 0, (cudaStream_t)stream, kv8::view(c), c->d_table,
+                         c->d_len, c->d_refs, n, d_parents, d_children, kv8::carve(c, n, d_ws));
 }
 
 extern "C" int tq_kv8_truncate(const tq_kv8_t* c, int n, const int32_t* d_slots,
                                const int32_t* d_lens, void* d_ws, size_t ws_bytes, void* stream) {
     const int rc = kv8::check_list(c, n, d_slots, d_lens, d_ws, ws_bytes);
     if (rc || n == 0) return rc;
-    kv8::k_truncate<<<1, kv8::kPT, 0, (cudaStream_t)stream>>>(kv8::view(c), c->d_table, c->d_len,
-                                                              c->d_refs, n, d_slots, d_lens,
-                                                              kv8::carve(c, n, d_ws));
-    TQ_CHECK_LAUNCH();
-    return TQ_OK;
+    return launch_behind(kv8::k_truncate, dim3(1), kv8::kPT, 0, (cudaStream_t)stream, kv8::view(c), c->d_table,
+                         c->d_len, c->d_refs, n, d_slots, d_lens, kv8::carve(c, n, d_ws));
 }
 
 extern "C" int tq_kv8_compact(const tq_kv8_t* c, void* d_ws, size_t ws_bytes, void* stream) {
-    const int rc = kv8::check_list(c, 0, nullptr, nullptr, d_ws, ws_bytes);
+    int rc = kv8::check_list(c, 0, nullptr, nullptr, d_ws, ws_bytes);
     if (rc) return rc;
     if (!d_ws || ws_bytes < kv8::pages_workspace(c, 0)) return TQ_ERR_WORKSPACE;
     const kv8::PagesWs w = kv8::carve(c, 0, d_ws);
     cudaStream_t s = (cudaStream_t)stream;
-    kv8::k_compact<<<1, kv8::kPT, 0, s>>>(kv8::view(c), c->d_refs, w);
-    TQ_CHECK_LAUNCH();
-    return kv8::copy_pages<true>(c, w, c->pages / 2 + 1, s);
+    rc = launch_behind(kv8::k_compact, dim3(1), kv8::kPT, 0, s, kv8::view(c), c->d_refs, w);
+    return rc ? rc : kv8::copy_pages<true>(c, w, c->pages / 2 + 1, s);
 }

@@ -160,6 +160,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort = &sm.abort;
     const int unit = blockIdx.x;
+    grid_begin();
 
     // ---- the batch's steps: a run of entries a thread, prefix over the block
     int64_t* pre = reinterpret_cast<int64_t*>(sm.kv);  // (before the operands are)
@@ -467,7 +468,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 float R = 0.f;
                 for (int p = (k0 >> a.v.page_log2) + tid; p <= (k1 - 1) >> a.v.page_log2 && k1 > k0; p += 128) {
                     const int pid = page_of(a.v, e.slot, p);
-                    if (pid >= 0) R = fmaxf(R, __ldg(a.vs + (int64_t)pid * a.v.heads + it.head));
+                    if (pid >= 0) R = fmaxf(R, a.vs[(int64_t)pid * a.v.heads + it.head]);
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
@@ -483,7 +484,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     if (tid < 16) {
                         const int key = (it.t0 + t) * kPT + 16 * (tid & 7);
                         const int pid = key < e.len ? page_of(a.v, e.slot, key >> a.v.page_log2) : -1;
-                        if (pid >= 0) x = __ldg((tid < 8 ? a.ks : a.vs) + (int64_t)pid * a.v.heads + it.head);
+                        if (pid >= 0) x = (tid < 8 ? a.ks : a.vs)[(int64_t)pid * a.v.heads + it.head];
                         else x = tid < 8 ? -1.f : 0.f;
                     }
                     return x;
@@ -658,6 +659,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
 template <int D, typename T>
 __global__ __launch_bounds__(256) void k_prompt_merge(const Attn a, const PromptParts parts, int blocks) {
     const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_begin();
     if (u == 0 && blockIdx.y == 0) {
         int st = 0;
         for (int i = threadIdx.x; i < blocks; i += 256) st |= parts.block_status[i] != 0;
@@ -707,15 +709,12 @@ __global__ __launch_bounds__(256) void k_prompt_merge(const Attn a, const Prompt
 template <int FMT, int D, typename T>
 int go(const Attn& a, const CUtensorMap& km, const CUtensorMap& vm, const PromptParts& p, int blocks,
        cudaStream_t s) {
-    auto kern = k_attn_prompt<FMT, D, T>;
     constexpr int smem = (int)sizeof(PSmem<D>) + 1024;
     static_assert(smem <= 232448, "shared memory of a block");
-    TQ_TRY_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    kern<<<blocks, kPThreads, smem, s>>>(a, km, vm, p);
-    TQ_CHECK_LAUNCH();
-    k_prompt_merge<D, T><<<dim3((unsigned)blocks, 16), 256, 0, s>>>(a, p, blocks);
-    TQ_CHECK_LAUNCH();
-    return TQ_OK;
+    int rc = allow_smem<k_attn_prompt<FMT, D, T>>(smem);
+    if (!rc) rc = launch_behind(k_attn_prompt<FMT, D, T>, dim3(blocks), kPThreads, smem, s, a, km, vm, p);
+    if (!rc) rc = launch_behind(k_prompt_merge<D, T>, dim3((unsigned)blocks, 16), 256, 0, s, a, p, blocks);
+    return rc;
 }
 
 template <int D>

@@ -10,7 +10,7 @@
 // by the launch for few.
 #include <cmath>
 
-#include "tq_internal.cuh"
+#include "tq_launch.cuh"
 #include "tq_rope.cuh"
 
 namespace tq {
@@ -41,11 +41,12 @@ struct alignas(sizeof(T) * VEC) Pack {
 // VEC = 1 an interleaved pair is two runs of one.
 template <typename T, int VEC>
 __global__ __launch_bounds__(kRT) void k_rope(const __grid_constant__ tq_rope_params_t r, int64_t T_,
-                                              int heads, const T* __restrict__ x, int64_t x_ts,
-                                              int64_t x_hs, const int64_t* __restrict__ pos, T* out,
+                                              int heads, const T* x, int64_t x_ts,
+                                              int64_t x_hs, const int64_t* pos, T* out,
                                               int64_t out_ts, int64_t out_hs, int transpose,
                                               int tokens, int in_place) {
     extern __shared__ float2 s_cs[];  // [tokens][rot/2]: a cos, a sin
+    grid_begin();
     using P = Pack<T, VEC>;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int nt = (int)min((int64_t)tokens, T_ - t0);
@@ -115,16 +116,9 @@ int launch(const tq_rope_params_t& r, int64_t T_, int heads, const void* x, int6
     const int64_t blocks = (T_ + tokens - 1) / tokens;
     if (blocks > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
     const size_t smem = (size_t)tokens * (r.rot / 2) * sizeof(float2);
-    if (wide)
-        k_rope<T, V><<<(unsigned)blocks, kRT, smem, s>>>(r, T_, heads, (const T*)x, x_ts, x_hs, pos,
-                                                         (T*)out, out_ts, out_hs, transpose, tokens,
-                                                         in_place);
-    else
-        k_rope<T, 1><<<(unsigned)blocks, kRT, smem, s>>>(r, T_, heads, (const T*)x, x_ts, x_hs, pos,
-                                                         (T*)out, out_ts, out_hs, transpose, tokens,
-                                                         in_place);
-    TQ_CHECK_LAUNCH();
-    return TQ_OK;
+    return launch_behind(wide ? k_rope<T, V> : k_rope<T, 1>, dim3((unsigned)blocks), kRT, smem, s, r, T_,
+                         heads, (const T*)x, x_ts, x_hs, pos, (T*)out, out_ts, out_hs, transpose, tokens,
+                         in_place);
 }
 
 }  // namespace

@@ -537,6 +537,16 @@ def test_attention_padded_batch(tq_lib, cuda, counts):
         assert want.shape[0] == used
 
 
+def test_attention_unaligned_queries(tq_lib, cuda):
+    """Packed projections whose rows do not begin at 16 bytes, one token and one
+    head among them (their strides count for nothing)."""
+    c = fill(tq_lib, cuda, "i8", 1, 64, 32, [90])
+    packed = torch.randn(4, 387, generator=gen(3)).to(torch.bfloat16).to(cuda)
+    for q in (packed[:1, :256].unflatten(1, (4, 64)), packed[:, 3:67].unsqueeze(1),
+              packed[:3, 1:257].unflatten(1, (4, 64)), packed[2:3, 64:128].unsqueeze(1)):
+        check_attention(c, q, [q.shape[0]], [90])
+
+
 @pytest.mark.parametrize("counts", [[5, 1], [90, 70]])
 def test_attention_widest_window(tq_lib, cuda, counts):
     """Windows beyond every length, up to the largest int, hide nothing; more
