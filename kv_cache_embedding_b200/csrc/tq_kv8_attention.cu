@@ -14,9 +14,11 @@
 // ragged lengths included -- and keeps kStages tiles of K and V in flight by TMA
 // into its private ring; warps meet only where an item's steps are cut, and
 // there k_attn_merge joins the parts in the order of their keys.  Products are
-// m16n8k16 MMAs on half fragments made in registers from the codes (K: plain
-// ldmatrix, coordinates permuted alike on both sides; V: transposing ldmatrix of
-// byte pairs, the halves sorted out by byte permutes).
+// m16n8k16 MMAs with the codes as the A operand (16 keys, then 16 coordinates)
+// and the query rows as the 8 columns: a code is converted once for all rows, and
+// 8 rows cost half of what 16 do.  Fragments are made in registers from the codes
+// (K: plain ldmatrix, coordinates permuted alike on both sides; V: transposing
+// ldmatrix of byte pairs, the halves sorted out by byte permutes).
 #include <cmath>
 #include <mutex>
 
@@ -58,14 +60,17 @@ int code_map(CUtensorMap* m, const void* base, int d, int64_t rows, int box) {
 namespace {
 
 constexpr int kTile = 32;     // keys a step
-constexpr int kRows = 16;     // query rows of an item (MMA M)
-constexpr int kWarps = 8;
-constexpr int kStages = 3;
+constexpr int kRows = 16;     // query rows of an item, at most
+constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
+template <int D>
+constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB of a warp's ring
 
 // Workspace: [status word (256 B) | a status word a block | a Cut a warp | per
 // warp two parts: (m, L) of 16 rows, 16 x d sums].  Part 2u: the end of an item
 // that warp u did not begin; 2u + 1: the beginning of one that it does not end.
+// (u counts all warps of the grid; a small batch keeps only the first
+// Cut::per_block warps of each block busy, so that it spreads over the SMs.)
 struct Parts {
     int* status;
     int* block_status;
@@ -76,15 +81,16 @@ struct Parts {
 
 template <int D>
 struct alignas(1024) WarpSmem {
-    uint8_t k[kStages][kTile * D];
-    uint8_t v[kStages][kTile * D];
+    uint8_t k[kStages<D>][kTile * D];
+    uint8_t v[kStages<D>][kTile * D];
 };
 template <int D>
 struct Smem {
     WarpSmem<D> w[kWarps];
-    float scale[kWarps][kStages][4];  // K of both halves of a tile, V of both; K -inf: no page
-    uint64_t full[kWarps][kStages];
-    int64_t pre[kThreads + 1];        // steps before each thread's run of entries
+    float scale[kWarps][kStages<D>][4];  // K of both halves of a tile, V of both; K -inf: no page
+    uint64_t full[kWarps][kStages<D>];
+    int64_t pre[kThreads + 1];           // steps before each thread's run of entries
+    int64_t sums[kWarps];
     int abort;
 };
 
@@ -106,6 +112,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of halves, transposed.
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -151,18 +163,22 @@ struct Place {
     }
 };
 
-template <int FMT, int D, typename T>
+// NB: blocks of 8 query rows.
+template <int FMT, int D, int NB, typename T>
 __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const __grid_constant__ CUtensorMap kmap,
                                                            const __grid_constant__ CUtensorMap vmap,
                                                            const Parts parts) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     constexpr int CH = D / 16;  // 16-byte chunks of a code row
+    constexpr int NS = kStages<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = warp * gridDim.x + blockIdx.x;  // short work spreads over the SMs
-    const int64_t umax = (int64_t)gridDim.x * kWarps;
+    const int self = blockIdx.x * kWarps + warp;
     WarpSmem<D>& ws = sm.w[warp];
     volatile int* abort = &sm.abort;
+    if (threadIdx.x == 0) sm.abort = 0;
+    if (lane < NS) mbar_init(&sm.full[warp][lane], 1);
+    fence_mbar_init();
     grid_begin();
 
     // ---- the batch's steps: a run of entries a thread, prefix over the block
@@ -171,32 +187,29 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         int64_t mine = 0;
         for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i)
             mine += span_of(a, i).steps;
-        if (threadIdx.x == 0) sm.abort = 0;
-        if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
-        fence_mbar_init();
         int64_t inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
+        if (lane == 31) sm.sums[warp] = inc;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) inc += sm.sums[w];
         sm.pre[threadIdx.x + 1] = inc;
-        __syncthreads();
-        int64_t before = 0;
-        for (int w = 0; w < warp; ++w) before += sm.pre[32 * w + 32];
-        __syncthreads();
-        sm.pre[threadIdx.x + 1] = inc + before;
         if (threadIdx.x == 0) sm.pre[0] = 0;
         __syncthreads();
     }
     const int64_t total = sm.pre[kThreads];
-    const int64_t units = min(umax, total);
+    const int busy = (int)min((int64_t)kWarps, max((int64_t)1, (total + gridDim.x - 1) / gridDim.x));
+    const int64_t units = min((int64_t)gridDim.x * busy, total);
+    const int64_t unit = (int64_t)blockIdx.x * busy + warp;
     int64_t g0 = 0, g1 = 0;
-    if (unit < units) {
+    if (warp < busy && unit < units) {
         g0 = unit * total / units;
         g1 = (unit + 1) * total / units;
     }
-    if (lane == 0) parts.cut[unit].parts = 0;
+    if (lane == 0) parts.cut[self].parts = 0;
 
     auto locate = [&](int64_t g, Place& p) {
         int lo = 0, hi = kThreads;  // the run that holds step g
@@ -216,16 +229,34 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         p.entry = i;
         p.open(rem);
     };
+    // On to the next step's place, over entries without steps.
+    auto advance = [&](Place& p) {
+        if (p.next(a.v.heads)) return;
+        int i = p.entry;
+        do {
+            p.s = span_of(a, ++i);
+        } while (p.s.steps == 0);
+        p.entry = i;
+        p.open(0);
+    };
 
-    // ---- producer: tile loads kStages - 1 ahead.  Lane j < 4 serves half j & 1
-    // of the tile (pages of 16 end inside it), K (j < 2) or V.
+    // ---- producer: tile loads NS - 1 ahead, page ids one further, scales into
+    // shared memory one tile later: nothing waits for a lookup.  Lane j < 4 serves
+    // half j & 1 of the tile (pages of 16 end inside it), K (j < 2) or V.
     Place pp = {};
     int64_t gp = g0;
-    int pstage = 0;
-    const int box = min(a.v.page, kTile);
-    const int nbox = kTile / box;
+    uint32_t np = 0;  // tiles produced
+    const int box = min(a.v.page, kTile), nbox = kTile / box;
+    const int hf = lane & 1, isv = lane >> 1;
+    int pid = -1;       // page of this lane's half of the next tile
     float pend = 0.f;   // the last produced tile's scale, on its way
     int pend_stage = -1;
+    auto lookup = [&]() {
+        if (lane < 4) {
+            const int key = (pp.s.tile0 + pp.t) * kTile + hf * 16;
+            pid = key < pp.s.e.len ? page_of(a.v, pp.s.e.slot, key >> a.v.page_log2) : -1;
+        }
+    };
     auto settle = [&]() {
         if (pend_stage >= 0 && lane < 4) sm.scale[warp][pend_stage][lane] = pend;
         pend_stage = -1;
@@ -233,33 +264,26 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     auto produce = [&]() {
         settle();
         if (gp >= g1) return;
-        uint64_t* bar = &sm.full[warp][pstage];
+        const int st = np % NS;
+        uint64_t* bar = &sm.full[warp][st];
         if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kTile * D);
         __syncwarp();
         if (lane < 4) {
-            const int hf = lane & 1, isv = lane >> 1;
             const int key = (pp.s.tile0 + pp.t) * kTile + hf * 16;
-            int pid = -1;
-            if (key < pp.s.e.len) pid = page_of(a.v, pp.s.e.slot, key >> a.v.page_log2);
             const int64_t ph = (int64_t)max(pid, 0) * a.v.heads + pp.head;
             if (hf < nbox) {
                 // an absent page reads as zeros: rows behind the tensor
                 const int row = pid >= 0 ? (int)((ph << a.v.page_log2) + (key & (a.v.page - 1))) : a.rows;
-                uint8_t* dst = (isv ? ws.v[pstage] : ws.k[pstage]) + hf * box * D;
+                uint8_t* dst = (isv ? ws.v[st] : ws.k[st]) + hf * box * D;
                 tma_load_2d(dst, isv ? &vmap : &kmap, 0, row, bar);
             }
             pend = pid < 0 ? (isv ? 0.f : -INFINITY) : (isv ? a.vs : a.ks)[ph];
         }
-        pend_stage = pstage;
-        pstage = pstage + 1 == kStages ? 0 : pstage + 1;
-        if (++gp < g1 && !pp.next(a.v.heads)) {
-            // the following entry with steps
-            int i = pp.entry;
-            do {
-                pp.s = span_of(a, ++i);
-            } while (pp.s.steps == 0);
-            pp.entry = i;
-            pp.open(0);
+        pend_stage = st;
+        ++np;
+        if (++gp < g1) {
+            advance(pp);
+            lookup();
         }
     };
 
@@ -268,11 +292,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     if (g0 < g1) {
         locate(g0, pp);
         p = pp;
+        lookup();
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) produce();
+        for (int s = 0; s < NS - 1; ++s) produce();
     }
-    int stage = 0;
-    uint32_t phase = 0;
+    uint32_t nc = 0;  // tiles consumed
     const int c2 = lane & 3, r0 = lane >> 2;
     // ldmatrix row of this lane: row lane % 8 of matrix lane / 8
     const int lrow = lane & 7, lmat = lane >> 3;
@@ -284,131 +308,148 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         const int t_end = (int)min((int64_t)p.s.tiles, t_begin + left);
         const Entry e = p.s.e;
         const int nrows = e.qn * a.group;
-        // rows r0 and r0 + 8 of this thread: query token, and the last key it sees
-        uint32_t qf[CH][4];
-        float sl[2], m[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
-        int lim[2], low[2];
+        // the query rows as MMA columns: this thread loads row 8 nb + r0, and keeps
+        // the sums of rows 8 nb + 2 c2 + {0, 1}: column 2 nb + {0, 1}
+        uint32_t qf[NB][CH][2];
+        float sl[2 * NB], m[2 * NB], L[2 * NB];
+        int lim[2 * NB], low[2 * NB];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = r0 + 8 * u;
-            const int ri = min(r, nrows - 1), tq = ri / a.group, hq = ri - tq * a.group;
+        for (int nb = 0; nb < NB; ++nb) {
+            const int ri = min(8 * nb + r0, nrows - 1), tq = ri / a.group, hq = ri - tq * a.group;
             const T* q = (const T*)a.q + (e.c0 + tq) * a.q_ts + (int64_t)(p.head * a.group + hq) * a.q_hs;
-            const int pos = e.len - e.qn + tq;
-            lim[u] = a.causal ? min(pos, e.len - 1) : e.len - 1;
-            low[u] = below_window(a, pos);
-            float x[CH][4], top = 0.f;
+            Pack<T, 4> v[CH];
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                const Pack<T, 4> v = *reinterpret_cast<const Pack<T, 4>*>(q + 16 * ch + 4 * c2);
+            for (int ch = 0; ch < CH; ++ch) v[ch] = *reinterpret_cast<const Pack<T, 4>*>(q + 16 * ch + 4 * c2);
+            float top = 0.f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[ch][k] = to_f(v.v[k]);
-                    top = fmaxf(top, fabsf(x[ch][k]));
-                }
-            }
+            for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(to_f(v[ch].v[k])));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const float unit_q = row_unit(top);
-            sl[u] = a.scale_log2 / unit_q;
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
-                qf[ch][u] = pack_half2(x[ch][0] * unit_q, x[ch][1] * unit_q);
-                qf[ch][u + 2] = pack_half2(x[ch][2] * unit_q, x[ch][3] * unit_q);
+                qf[nb][ch][0] = pack_half2(to_f(v[ch].v[0]) * unit_q, to_f(v[ch].v[1]) * unit_q);
+                qf[nb][ch][1] = pack_half2(to_f(v[ch].v[2]) * unit_q, to_f(v[ch].v[3]) * unit_q);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int u = 2 * nb + j, r = min(8 * nb + 2 * c2 + j, nrows - 1);
+                const int pos = e.len - e.qn + r / a.group;
+                sl[u] = a.scale_log2 / __shfl_sync(0xffffffffu, unit_q, 4 * (2 * c2 + j));
+                lim[u] = a.causal ? min(pos, e.len - 1) : e.len - 1;
+                low[u] = below_window(a, pos);
+                m[u] = -INFINITY;
+                L[u] = 0.f;
             }
         }
         // keys below `clear` and above `low_any` need no mask for any row
         const int clear = a.causal ? min(e.len - e.qn, e.len - 1) : e.len - 1;
-        const int low_any = a.window > 0 ? e.len - 1 - a.window : -1;
-        float o[2 * CH][4];  // chunk, parity: coordinates 16 ch + 4 c2 + 2 {0, 1} + parity
+        const int low_any = below_window(a, e.len - 1);
+        float o[NB][CH][4];  // coordinates 16 ch + 2 r0 + {0, 1} of the columns {0, 1}: [coordinate][column]
 #pragma unroll
-        for (int i = 0; i < 2 * CH; ++i)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[nb][i][k] = 0.f;
         float R = 0.f;  // running largest value scale: o is in units of it
 
         for (int t = t_begin; t < t_end; ++t) {
             const int key0 = (p.s.tile0 + t) * kTile;
-            settle();
-            if (!mbar_wait(&sm.full[warp][stage], phase, abort, kWaitNs)) ok = false;
+            produce();
+            const int stage = nc % NS;
+            if (!mbar_wait(&sm.full[warp][stage], (nc / NS) & 1, abort, kWaitNs)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            ++nc;
             const float4 sc = *reinterpret_cast<const float4*>(sm.scale[warp][stage]);
-            // ---- logits: 4 blocks of 8 keys
-            float s[4][4];
+            // ---- logits: 2 blocks of 16 keys; s[..][k]: key r0 + 8 (k / 2), column k & 1
+            float s[NB][2][4];
             const uint32_t kb = smem_u32(ws.k[stage]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s[b][k] = 0.f;
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int c = 0; c < CH; c += 4) {
-                    uint32_t w[4];
-                    ldsm4(kb + swz<D>(8 * b + lrow, c + lmat), w);
+                    for (int k = 0; k < 4; ++k) s[nb][b][k] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t lo, hi;
-                        codes_to_half<FMT>(w[k], lo, hi);
-                        mma16816(s[b], qf[c + k], lo, hi);
+                for (int c = 0; c < CH; c += 2) {
+                    uint32_t w[4];  // keys 0-7 | 8-15 of chunk c, then of chunk c + 1
+                    ldsm4(kb + swz<D>(16 * b + 8 * (lmat & 1) + lrow, c + (lmat >> 1)), w);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t f[4];
+                        codes_to_half<FMT>(w[2 * h], f[0], f[2]);
+                        codes_to_half<FMT>(w[2 * h + 1], f[1], f[3]);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) mma16816(s[nb][b], f, qf[nb][c + h][0], qf[nb][c + h][1]);
                     }
                 }
             }
             const bool masked = key0 + kTile - 1 > clear || key0 <= low_any || sc.x == -INFINITY ||
                                 sc.y == -INFINITY;
-            float mx[2] = {m[0], m[1]};
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const float ks = b < 2 ? sc.x : sc.y;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int u = k >> 1;
-                    float l = s[b][k] * (sl[u] * ks);
-                    if (masked) {
-                        const int key = key0 + 8 * b + 2 * c2 + (k & 1);
-                        if (key > lim[u] || key <= low[u] || ks == -INFINITY) l = -INFINITY;
-                    }
-                    s[b][k] = l;
-                    mx[u] = fmaxf(mx[u], l);
-                }
-            }
-            float alpha[2];
             const float vmax = fmaxf(sc.z, sc.w);
             const float shrink = vmax > R ? R / vmax : 1.f;
             R = fmaxf(R, vmax);
             // (scales below fp32's normal range have no reciprocal: their values count as 0)
             const float inv = R >= 1.17549435e-38f ? 1.f / R : 0.f;
-            const float w0 = sc.z * inv, w1 = sc.w * inv;
+            const float w[2] = {sc.z * inv, sc.w * inv};
+            uint32_t pf[NB][2][2];
+            float alpha[2 * NB];
+            bool rescale = false;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
-                mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
-                const float base = mx[u] == -INFINITY ? 0.f : mx[u];
-                alpha[u] = ex2(m[u] - base);
-                m[u] = mx[u];
-                mx[u] = base;
-                L[u] *= alpha[u];
-                alpha[u] *= shrink;
-            }
-            uint32_t pf[2][4];
+            for (int nb = 0; nb < NB; ++nb) {
+                float mx[2] = {m[2 * nb], m[2 * nb + 1]};
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const float w = b < 2 ? w0 : w1;
-                float pr[4];
+                for (int b = 0; b < 2; ++b) {
+                    const float ks = b == 0 ? sc.x : sc.y;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    pr[k] = ex2(s[b][k] - mx[k >> 1]);
-                    L[k >> 1] += pr[k];
+                    for (int k = 0; k < 4; ++k) {
+                        const int u = 2 * nb + (k & 1);
+                        float l = s[nb][b][k] * (sl[u] * ks);
+                        if (masked) {
+                            const int key = key0 + 16 * b + r0 + 8 * (k >> 1);
+                            if (key > lim[u] || key <= low[u] || ks == -INFINITY) l = -INFINITY;
+                        }
+                        s[nb][b][k] = l;
+                        mx[k & 1] = fmaxf(mx[k & 1], l);
+                    }
                 }
-                pf[b >> 1][2 * (b & 1)] = pack_half2(pr[0] * w, pr[1] * w);
-                pf[b >> 1][2 * (b & 1) + 1] = pack_half2(pr[2] * w, pr[3] * w);
-            }
-            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-                for (int i = 0; i < 2 * CH; ++i) {
-                    o[i][0] *= alpha[0];
-                    o[i][1] *= alpha[0];
-                    o[i][2] *= alpha[1];
-                    o[i][3] *= alpha[1];
+                for (int j = 0; j < 2; ++j) {
+                    const int u = 2 * nb + j;
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], x));
+                    const float base = mx[j] == -INFINITY ? 0.f : mx[j];
+                    alpha[u] = ex2(m[u] - base);
+                    m[u] = mx[j];
+                    mx[j] = base;
+                    L[u] *= alpha[u];
+                    alpha[u] *= shrink;
+                    rescale |= alpha[u] != 1.f;
                 }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float pr[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        pr[k] = ex2(s[nb][b][k] - mx[k & 1]);
+                        L[2 * nb + (k & 1)] += pr[k];
+                    }
+                    // keys x columns, transposed into the B operand
+                    pf[nb][b][0] = movm(pack_half2(pr[0] * w[b], pr[1] * w[b]));
+                    pf[nb][b][1] = movm(pack_half2(pr[2] * w[b], pr[3] * w[b]));
+                }
+            }
+            if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int i = 0; i < CH; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[nb][i][k] *= alpha[2 * nb + (k & 1)];
             }
             // e4m3 rows behind the slot's end may hold NaN codes, and 0 NaN is NaN
             if (FMT == TQ_KV_E4M3 && key0 + kTile > e.len) {
@@ -421,171 +462,176 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             // ---- values: 16 keys x 32 coordinates a load
             const uint32_t vb = smem_u32(ws.v[stage]);
 #pragma unroll
-            for (int k16 = 0; k16 < 2; ++k16) {
+            for (int b = 0; b < 2; ++b) {
 #pragma unroll
                 for (int c = 0; c < CH; c += 2) {
-                    uint32_t w[4];  // keys 0-7 | 8-15 of chunk c, then of chunk c + 1
-                    ldsm4t(vb + swz<D>(16 * k16 + 8 * (lmat & 1) + lrow, c + (lmat >> 1)), w);
+                    uint32_t x[4];  // keys 0-7 | 8-15 of chunk c, then of chunk c + 1
+                    ldsm4t(vb + swz<D>(16 * b + 8 * (lmat & 1) + lrow, c + (lmat >> 1)), x);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t e0, e1, d0, d1;
-                        codes_to_half_02<FMT>(w[2 * h], e0, d0);
-                        codes_to_half_02<FMT>(w[2 * h + 1], e1, d1);
-                        mma16816(o[2 * (c + h)], pf[k16], e0, e1);
-                        mma16816(o[2 * (c + h) + 1], pf[k16], d0, d1);
+                        uint32_t f[4];  // even coordinates, odd ones; the same of keys 8-15
+                        codes_to_half_02<FMT>(x[2 * h], f[0], f[1]);
+                        codes_to_half_02<FMT>(x[2 * h + 1], f[2], f[3]);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][c + h], f, pf[nb][b][0], pf[nb][b][1]);
                     }
                 }
             }
             __syncwarp();  // every lane is done with the stage
-            if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1;
-            }
-            produce();
         }
         if (!ok) break;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            L[u] += __shfl_xor_sync(0xffffffffu, L[u], 1);
-            L[u] += __shfl_xor_sync(0xffffffffu, L[u], 2);
-        }
         const bool begins = t_begin == 0, ends = t_end == p.s.tiles;
-        if (begins && ends) {
+        const int64_t slot = 2 * (int64_t)self + (begins ? 1 : 0);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int r = r0 + 8 * u;
-                if (r >= nrows) continue;
+        for (int u = 0; u < 2 * NB; ++u) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) L[u] += __shfl_xor_sync(0xffffffffu, L[u], x);
+            const int r = 8 * (u >> 1) + 2 * c2 + (u & 1), j = u & 1, nb = u >> 1;
+            if (r >= nrows) continue;
+            if (begins && ends) {
                 const int64_t tok = e.c0 + r / a.group;
                 const int hq = p.head * a.group + r % a.group;
                 const float n = L[u] > 0.f ? R / L[u] : (L[u] == 0.f ? 0.f : L[u]);
-                T* out = (T*)a.out + (tok * a.heads_q + hq) * D;
+                T* out = (T*)a.out + (tok * a.heads_q + hq) * D + 2 * r0;
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
-                    Pack<T, 4> v;
-                    from_f(o[2 * ch][2 * u] * n, v.v[0]);
-                    from_f(o[2 * ch + 1][2 * u] * n, v.v[1]);
-                    from_f(o[2 * ch][2 * u + 1] * n, v.v[2]);
-                    from_f(o[2 * ch + 1][2 * u + 1] * n, v.v[3]);
-                    *reinterpret_cast<Pack<T, 4>*>(out + 16 * ch + 4 * c2) = v;
+                    Pack<T, 2> v;
+                    from_f(o[nb][ch][j] * n, v.v[0]);
+                    from_f(o[nb][ch][2 + j] * n, v.v[1]);
+                    *reinterpret_cast<Pack<T, 2>*>(out + 16 * ch) = v;
                 }
-                if (a.lse && c2 == 0)
+                if (a.lse && r0 == 0)
                     a.lse[tok * a.heads_q + hq] = L[u] > 0.f ? (m[u] + log2f(L[u])) * 0.69314718056f : m[u];
-            }
-        } else {
-            const int64_t slot = 2 * (int64_t)unit + (begins ? 1 : 0);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int r = r0 + 8 * u;
-                if (r >= nrows) continue;
-                if (c2 == 0) parts.ml[slot * kRows + r] = make_float2(m[u], L[u]);
-                float* dst = parts.o + (slot * kRows + r) * D;
+            } else {
+                if (r0 == 0) parts.ml[slot * kRows + r] = make_float2(m[u], L[u]);
+                float* dst = parts.o + (slot * kRows + r) * D + 2 * r0;
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch)
-                    *reinterpret_cast<float4*>(dst + 16 * ch + 4 * c2) =
-                        make_float4(o[2 * ch][2 * u] * R, o[2 * ch + 1][2 * u] * R,
-                                    o[2 * ch][2 * u + 1] * R, o[2 * ch + 1][2 * u + 1] * R);
+                    *reinterpret_cast<float2*>(dst + 16 * ch) =
+                        make_float2(o[nb][ch][j] * R, o[nb][ch][2 + j] * R);
             }
-            if (begins && lane == 0) {
-                const int64_t last = g + p.s.tiles - 1;  // the item's last step: its warp
-                Cut c;
-                c.parts = (int)(((last + 1) * units - 1) / total) - unit + 1;
-                c.rows = nrows;
-                c.head = p.head;
-                c.pad = 0;
-                c.row0 = e.c0 * a.group;
-                parts.cut[unit] = c;
-            }
+        }
+        if (begins && !ends && lane == 0) {
+            const int64_t last = g + p.s.tiles - 1;  // the item's last step: its warp
+            Cut c;
+            c.parts = (int)(((last + 1) * units - 1) / total - unit + 1);
+            c.rows = nrows;
+            c.head = p.head;
+            c.per_block = busy;
+            c.row0 = e.c0 * a.group;
+            parts.cut[self] = c;
         }
         g += t_end - t_begin;
         if (g < g1) {
             p.t = p.s.tiles - 1;
-            if (!p.next(a.v.heads)) {
-                int i = p.entry;
-                do {
-                    p.s = span_of(a, ++i);
-                } while (p.s.steps == 0);
-                p.entry = i;
-                p.open(0);
-            }
+            advance(p);
         }
     }
     if (!ok) {
-        // gave up: no copy of this warp's ring may land after it has left
+        // gave up: no copy into this warp's ring may land after it has left
         *abort = 1;
-        for (int s = 0; s < kStages; ++s) mbar_wait(&sm.full[warp][s], phase, abort, kWaitNs);
+        int none = 0;
+        for (; nc < np; ++nc) mbar_wait(&sm.full[warp][nc % NS], (nc / NS) & 1, &none, kWaitNs);
     }
     __syncthreads();
     if (threadIdx.x == 0) parts.block_status[blockIdx.x] = sm.abort ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 80 : 0;
 }
 
-// Joins the parts of the items that were cut: block (u, r) row r of the item
-// that begins in warp u and does not end there.  4 warps take every fourth part.
+// Joins the parts of the items that were cut: block u the item that begins in
+// warp u and does not end there.  8 warps share the rows, and the parts of a row.
+constexpr int kMergeWarps = 8;
 template <int D, typename T>
-__global__ __launch_bounds__(128) void k_attn_merge(const Attn a, const Parts parts, int blocks) {
-    const int u = blockIdx.x, r = blockIdx.y;
+__global__ __launch_bounds__(32 * kMergeWarps) void k_attn_merge(const Attn a, const Parts parts, int blocks) {
+    __shared__ float s_m[kMergeWarps], s_L[kMergeWarps];
+    __shared__ float s_o[kMergeWarps][D];
     grid_begin();
-    if (u == 0 && r == 0) {  // the call's status
+    const int u = blockIdx.x;
+    if (u == 0) {  // the call's status
         int st = 0;
-        for (int i = threadIdx.x; i < blocks; i += 128) st = min(st, parts.block_status[i]);
+        for (int i = threadIdx.x; i < blocks; i += 32 * kMergeWarps) st = min(st, parts.block_status[i]);
         st = __syncthreads_or(st);
         if (threadIdx.x == 0) *parts.status = st ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 80 : 0;
     }
     const Cut c = parts.cut[u];
-    if (c.parts == 0 || r >= c.rows) return;
-    __shared__ float s_ml[4][2];
-    __shared__ float s_o[4][D];
+    if (c.parts == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int E = D / 32;
-    // part i of the item: 2u + 1 first, then 2 (u + i)
-    auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)u + 1 : 2 * (int64_t)(u + i); };
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < c.parts; i += 128) m = fmaxf(m, parts.ml[slot(i) * kRows + r].x);
+    // part i of the item: 2u + 1 first, then part 2v of the i-th busy warp v behind u
+    const int block = u / kWarps, first = u % kWarps;
+    auto slot = [&](int i) {
+        const int w = first + i, b = w / c.per_block;
+        return i == 0 ? 2 * (int64_t)u + 1 : 2 * ((int64_t)(block + b) * kWarps + w - b * c.per_block);
+    };
+    // per: warps that share a row
+    const int per = c.rows == 1 ? 8 : c.rows == 2 ? 4 : c.rows <= 4 ? 2 : 1;
+    for (int r0 = 0; r0 < c.rows; r0 += kMergeWarps / per) {
+        const int r = r0 + warp / per, sub = warp % per;
+        float m = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) s_ml[warp][0] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_ml[0][0], s_ml[1][0]), fmaxf(s_ml[2][0], s_ml[3][0]));
-    const float base = m == -INFINITY ? 0.f : m;
-    float L = 0.f, acc[E];
+        for (int k = 0; k < E; ++k) acc[k] = 0.f;
+        if (r < c.rows) {
+            for (int i = sub + lane * per; i < c.parts; i += 32 * per) m = fmaxf(m, parts.ml[slot(i) * kRows + r].x);
 #pragma unroll
-    for (int k = 0; k < E; ++k) acc[k] = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < c.parts; i += 4) {
-        const float2 ml = parts.ml[slot(i) * kRows + r];
-        const float w = ex2(ml.x - base);
-        L = fmaf(w, ml.y, L);
-        const float* src = parts.o + (slot(i) * kRows + r) * D + lane * E;
-        float x[E];
-        if (E == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
-        else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+            for (int i = sub; i < c.parts; i += per) {
+                const int64_t pr = slot(i) * kRows + r;
+                const float2 ml = parts.ml[pr];
+                const float* src = parts.o + pr * D + lane * E;
+                float x[E];
+                if (E == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+                else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+                const float w = ex2(ml.x - base);
+                L = fmaf(w, ml.y, L);
 #pragma unroll
-        for (int k = 0; k < E; ++k) acc[k] = fmaf(w, x[k], acc[k]);
+                for (int k = 0; k < E; ++k) acc[k] = fmaf(w, x[k], acc[k]);
+            }
+        }
+        if (per > 1) {
+            if (lane == 0) {
+                s_m[warp] = m;
+                s_L[warp] = L;
+            }
+#pragma unroll
+            for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = acc[k];
+            __syncthreads();
+            if (sub == 0 && r < c.rows) {
+                float top = -INFINITY;
+                for (int w = warp; w < warp + per; ++w) top = fmaxf(top, s_m[w]);
+                const float base = top == -INFINITY ? 0.f : top;
+                L = 0.f;
+#pragma unroll
+                for (int k = 0; k < E; ++k) acc[k] = 0.f;
+                for (int w = warp; w < warp + per; ++w) {
+                    const float f = ex2(s_m[w] - base);
+                    L = fmaf(f, s_L[w], L);
+#pragma unroll
+                    for (int k = 0; k < E; ++k) acc[k] = fmaf(f, s_o[w][lane * E + k], acc[k]);
+                }
+                m = top;
+            }
+        }
+        if (sub == 0 && r < c.rows) {
+            const int64_t ri = c.row0 + r, tok = ri / a.group;
+            const int hq = c.head * a.group + (int)(ri % a.group);
+            const float n = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+            Pack<T, E> y;
+#pragma unroll
+            for (int k = 0; k < E; ++k) from_f(acc[k] * n, y.v[k]);
+            *reinterpret_cast<Pack<T, E>*>((T*)a.out + (tok * a.heads_q + hq) * D + lane * E) = y;
+            if (a.lse && lane == 0)
+                a.lse[tok * a.heads_q + hq] = L > 0.f ? (m + log2f(L)) * 0.69314718056f : m;
+        }
     }
-    if (lane == 0) s_ml[warp][1] = L;
-#pragma unroll
-    for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = acc[k];
-    __syncthreads();
-    L = s_ml[0][1] + s_ml[1][1] + s_ml[2][1] + s_ml[3][1];
-    const int64_t ri = c.row0 + r, tok = ri / a.group;
-    const int hq = c.head * a.group + (int)(ri % a.group);
-    const float n = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    if (threadIdx.x < D) {
-        const float x = s_o[0][threadIdx.x] + s_o[1][threadIdx.x] + s_o[2][threadIdx.x] + s_o[3][threadIdx.x];
-        from_f(x * n, ((T*)a.out)[(tok * a.heads_q + hq) * D + threadIdx.x]);
-    }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[tok * a.heads_q + hq] = L > 0.f ? (m + log2f(L)) * 0.69314718056f : m;
 }
 
 constexpr int kMaxBlocks = 148;  // the workspace's size
 
 // The most steps that a call of these sizes can have (its lengths lie on the
 // device); blocks: one an SM, fewer where the tables are too short to fill them.
-int64_t most_steps(const tq_kv8_t* c, int ns) {
-    return ((int64_t)c->max_pages * c->page + kTile - 1) / kTile * ns * c->heads;
-}
 int64_t blocks_for(const tq_kv8_t* c, int ns) {
-    const int64_t steps = most_steps(c, ns);
+    const int64_t steps = ((int64_t)c->max_pages * c->page + kTile - 1) / kTile * ns * c->heads;
     return steps < kMaxBlocks ? (steps < 1 ? 1 : steps) : kMaxBlocks;
 }
 
@@ -619,27 +665,32 @@ Parts carve(void* ws, int64_t blocks, size_t* bytes) {
     return p;
 }
 
-template <int FMT, int D, typename T>
+template <int FMT, int D, int NB, typename T>
 int launch(const Attn& a, const CUtensorMap& km, const CUtensorMap& vm, const Parts& p, int blocks,
-           int cuts, int rows, cudaStream_t s) {
+           cudaStream_t s) {
     constexpr int smem = (int)sizeof(Smem<D>) + 1024;
-    int rc = allow_smem<k_attn_rows<FMT, D, T>>(smem);
-    if (!rc) rc = launch_behind(k_attn_rows<FMT, D, T>, dim3(blocks), kThreads, smem, s, a, km, vm, p);
-    if (!rc)
-        rc = launch_behind(k_attn_merge<D, T>, dim3((unsigned)cuts, (unsigned)rows), 128, 0, s, a, p, blocks);
+    static_assert(smem <= 232448, "shared memory of a block");
+    int rc = allow_smem<k_attn_rows<FMT, D, NB, T>>(smem);
+    if (!rc) rc = launch_behind(k_attn_rows<FMT, D, NB, T>, dim3(blocks), kThreads, smem, s, a, km, vm, p);
+    if (!rc) rc = launch_behind(k_attn_merge<D, T>, dim3(blocks * kWarps), 32 * kMergeWarps, 0, s, a, p, blocks);
     return rc;
+}
+
+template <int FMT, int D, typename T>
+int launch_rows(const Attn& a, const CUtensorMap& km, const CUtensorMap& vm, const Parts& p, int blocks,
+                int rows, cudaStream_t s) {
+    return rows <= 8 ? launch<FMT, D, 1, T>(a, km, vm, p, blocks, s)
+                     : launch<FMT, D, 2, T>(a, km, vm, p, blocks, s);
 }
 
 template <int D>
 int dispatch(const tq_kv8_t* c, const Attn& a, const CUtensorMap& km, const CUtensorMap& vm,
-             const Parts& p, int blocks, int cuts, int rows, int q_dtype, cudaStream_t s) {
+             const Parts& p, int blocks, int rows, int q_dtype, cudaStream_t s) {
     if (c->format == TQ_KV_I8)
-        return q_dtype == TQ_BF16
-                   ? launch<TQ_KV_I8, D, __nv_bfloat16>(a, km, vm, p, blocks, cuts, rows, s)
-                   : launch<TQ_KV_I8, D, __half>(a, km, vm, p, blocks, cuts, rows, s);
-    return q_dtype == TQ_BF16
-               ? launch<TQ_KV_E4M3, D, __nv_bfloat16>(a, km, vm, p, blocks, cuts, rows, s)
-               : launch<TQ_KV_E4M3, D, __half>(a, km, vm, p, blocks, cuts, rows, s);
+        return q_dtype == TQ_BF16 ? launch_rows<TQ_KV_I8, D, __nv_bfloat16>(a, km, vm, p, blocks, rows, s)
+                                  : launch_rows<TQ_KV_I8, D, __half>(a, km, vm, p, blocks, rows, s);
+    return q_dtype == TQ_BF16 ? launch_rows<TQ_KV_E4M3, D, __nv_bfloat16>(a, km, vm, p, blocks, rows, s)
+                              : launch_rows<TQ_KV_E4M3, D, __half>(a, km, vm, p, blocks, rows, s);
 }
 
 Parts carve_for(const tq_kv8_t* c, void* ws, int64_t blocks, size_t* bytes) {
@@ -702,7 +753,8 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
     a.rows = c->pages * c->heads * c->page;
     cudaStream_t s = (cudaStream_t)stream;
     const bool few = kv8::any_few(c, ns, total_q, max_q, heads_q);
-    a.few = few ? kv8::kRows : 0;
+    const int64_t most = (int64_t)max_q * a.group;
+    a.few = few ? (int)(most < kv8::kRows ? most : kv8::kRows) : 0;
     size_t at = 256;
     if (few) {
         const int box = c->page < kv8::kTile ? c->page : kv8::kTile;
@@ -712,12 +764,8 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
         if (rc) return rc;
         const int blocks = (int)kv8::blocks_for(c, ns);
         const kv8::Parts p = kv8::carve_for(c, d_ws, blocks, &at);
-        const int64_t steps = kv8::most_steps(c, ns);
-        const int cuts = (int)(steps < blocks * kv8::kWarps ? steps : blocks * kv8::kWarps);
-        const int64_t most = (int64_t)max_q * a.group;
-        const int rows = (int)(most < kv8::kRows ? most : kv8::kRows);
-        rc = c->d == 128 ? kv8::dispatch<128>(c, a, km, vm, p, blocks, cuts, rows, q_dtype, s)
-                         : kv8::dispatch<64>(c, a, km, vm, p, blocks, cuts, rows, q_dtype, s);
+        rc = c->d == 128 ? kv8::dispatch<128>(c, a, km, vm, p, blocks, a.few, q_dtype, s)
+                         : kv8::dispatch<64>(c, a, km, vm, p, blocks, a.few, q_dtype, s);
         if (rc) return rc;
     }
     if (!kv8::any_many(c, max_q, heads_q)) return TQ_OK;

@@ -31,7 +31,7 @@ struct Attn {
 struct Cut {
     int parts;       // streams that share the item which begins here; 0: none
     int rows, head;  // its rows and KV head
-    int pad;
+    int per_block;   // few-rows kernel: busy warps of a block
     int64_t row0;    // its first row of the entry's (token x group) rows, from token 0
 };
 
