@@ -507,8 +507,9 @@ TQ_API int tq_kv8_read(const tq_kv8_t *c, int layer, int ns, const int32_t *d_sl
  * contiguous.  d_lse: [total_q][heads_q] fp32 or NULL.  heads_q a multiple of
  * heads, at most 128 times as many (else TQ_ERR_UNSUPPORTED).
  * d_ws: >= tq_kv8_workspace_bytes(TQ_KV8_OP_ATTENTION, c, ns, total_q, max_q,
- * heads_q); calls that overlap on the GPU need workspaces of their own.  The
- * result does not depend on what else runs, nor on earlier calls. */
+ * heads_q), any contents; calls that overlap on the GPU need workspaces of their
+ * own.  The result does not depend on what else runs, nor on earlier calls.  A
+ * captured call that has timed out is to be captured anew. */
 TQ_API int tq_kv8_attention(const tq_kv8_t *c, int layer, int ns, const int32_t *d_slots,
                             const int32_t *d_cu, int64_t total_q, int max_q, int heads_q,
                             const void *d_q, int q_dtype, int64_t q_ts, int64_t q_hs, float scale,

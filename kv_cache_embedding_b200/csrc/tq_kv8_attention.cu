@@ -12,13 +12,15 @@
 // 16 rows), so every warp is a stream of its own: it takes an equal, contiguous
 // share of all (entry, head, 32-key tile) steps of the batch --
 // ragged lengths included -- and keeps kStages tiles of K and V in flight by TMA
-// into its private ring; warps meet only where an item's steps are cut, and
-// there k_attn_merge joins the parts in the order of their keys.  Products are
+// into its private ring; warps meet only where an item's steps are cut (joining
+// the parts, below).  Products are
 // m16n8k16 MMAs with the codes as the A operand (16 keys, then 16 coordinates)
 // and the query rows as the 8 columns: a code is converted once for all rows, and
 // 8 rows cost half of what 16 do.  Fragments are made in registers from the codes
 // (K: plain ldmatrix, coordinates permuted alike on both sides; V: transposing
 // ldmatrix of byte pairs, the halves sorted out by byte permutes).
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <mutex>
 
@@ -63,20 +65,43 @@ constexpr int kTile = 32;     // keys a step
 constexpr int kRows = 16;     // query rows of an item, at most
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kItemTiles = 4 * kWarps;  // see "sharing out"
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB of a warp's ring
 
-// Workspace: [status word (256 B) | a status word a block | a Cut a warp | per
-// warp two parts: (m, L) of 16 rows, 16 x d sums].  Part 2u: the end of an item
-// that warp u did not begin; 2u + 1: the beginning of one that it does not end.
-// (u counts all warps of the grid; a small batch keeps only the first
-// Cut::per_block warps of each block busy, so that it spreads over the SMs.)
+// Sharing out.  A small batch (no more items than blocks, none of more than
+// kItemTiles tiles) takes a block an item.  Otherwise every warp takes an equal,
+// contiguous share of the steps; few steps keep only the first `busy` warps of each
+// block at work, so that they spread over the SMs.  "Unit" u is warp u % busy of
+// block u / busy.
+//
+// Joining.  Parts of an item that lies within a block meet in shared memory (the
+// ring of a warp that is through), or in the workspace where their warp goes on
+// with another item.  Of an item across blocks every part goes to the workspace
+// (part 2w: the end or middle of an item that warp w did not begin, 2w + 1 the
+// beginning of one), a block sets its flag behind the parts of the one item that
+// goes on beyond it, and the block in which the item ends waits for the flags of
+// the others -- blocks before it, which are dispatched before it -- and joins.  A
+// flag is set to the call's nonce and taken back by the joining block, so a
+// workspace needs no preparation and a replayed graph finds none set.  The order
+// of the sum is that of the keys.
+//
+// Workspace: [status word (256 B) | a flag a block | per warp two parts: (m, L) of
+// 16 rows, 16 x d sums].
 struct Parts {
     int* status;
-    int* block_status;
-    Cut* cut;
+    uint64_t* flag;
     float2* ml;
     float* o;
+    uint64_t nonce;
+};
+
+// An item whose parts are to be joined.
+struct Job {
+    int64_t row0;   // its first row of the entry's (token x group) rows, from token 0
+    int64_t first;  // the unit that begins it
+    int parts;      // units that hold a part; 0: no job
+    int rows, head;
 };
 
 template <int D>
@@ -90,7 +115,13 @@ struct Smem {
     float scale[kWarps][kStages<D>][4];  // K of both halves of a tile, V of both; K -inf: no page
     uint64_t full[kWarps][kStages<D>];
     int64_t pre[kThreads + 1];           // steps before each thread's run of entries
-    int64_t sums[kWarps];
+    int items[kThreads + 1];             // items before it
+    int64_t warp_steps[kWarps];
+    int warp_items[kWarps], warp_most[kWarps];
+    float2 ml[kWarps][kRows];            // of the part that a warp leaves in its ring
+    Job own[kWarps], early;              // items within the block, by their first warp; begun before it
+    int outside[kWarps];                 // the end of an own item that this warp left in the workspace
+    int beyond;                          // an item goes on behind the block
     int abort;
 };
 
@@ -131,6 +162,12 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
                     : (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
 }
 
+// Quotient of non-negative numbers; 64-bit division is a subroutine of some
+// hundred cycles, and the numbers mostly fit 32.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Steps of batch entry i: heads x tiles (one tile at least, so that rows without
 // keys are written); none where it has no rows, or too many for this kernel.
 struct Span {
@@ -153,7 +190,7 @@ struct Place {
     Span s;
     int entry, head, t;  // t: tile within the item
     __device__ __forceinline__ void open(int64_t rem) {
-        head = (int)(rem / s.tiles);
+        head = (int)quot(rem, s.tiles);
         t = (int)(rem - (int64_t)head * s.tiles);
     }
     __device__ __forceinline__ bool next(int heads) {  // false: the entry is through
@@ -162,6 +199,72 @@ struct Place {
         return ++head < heads;
     }
 };
+
+__device__ __forceinline__ void set_flag(uint64_t* p, uint64_t x) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(x) : "memory");
+}
+__device__ __forceinline__ uint64_t get_flag(const uint64_t* p) {
+    uint64_t x;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(p) : "memory");
+    return x;
+}
+template <int D>
+struct Sum {
+    float m, L, acc[D / 32];  // coordinates lane * D / 32 ..
+};
+// Every `step`-th of n parts of a row, from part i0 on: a warp.  ml(i), o(i):
+// where part i lies.
+template <int D, typename Ml, typename O>
+__device__ __forceinline__ Sum<D> sum_parts(int n, int i0, int step, int lane, Ml ml, O o) {
+    constexpr int E = D / 32;
+    Sum<D> s;
+    s.m = -INFINITY;
+    s.L = 0.f;
+#pragma unroll
+    for (int k = 0; k < E; ++k) s.acc[k] = 0.f;
+    for (int c0 = i0; c0 < n; c0 += 32 * step) {  // 32 parts: (m, L) of one a lane
+        const int mine = c0 + lane * step;
+        const float2 x = mine < n ? ml(mine) : make_float2(-INFINITY, 0.f);
+        float m = fmaxf(s.m, x.x);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const float base = m == -INFINITY ? 0.f : m;
+        const float w = ex2(x.x - base), old = ex2(s.m - base);
+        float L = w * x.y;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+        s.L = fmaf(s.L, old, L);
+        s.m = m;
+#pragma unroll
+        for (int k = 0; k < E; ++k) s.acc[k] *= old;
+        const int cnt = min(32, (n - c0 + step - 1) / step);
+#pragma unroll 4
+        for (int i = 0; i < cnt; ++i) {
+            const float* src = o(c0 + i * step) + lane * E;
+            float y[E];
+            if (E == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(src);
+            else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(src);
+            const float f = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+            for (int k = 0; k < E; ++k) s.acc[k] = fmaf(f, y[k], s.acc[k]);
+        }
+    }
+    return s;
+}
+template <int D, typename T>
+__device__ __forceinline__ void write_row(const Attn& a, const Job& job, int r, const Sum<D>& s, int lane) {
+    constexpr int E = D / 32;
+    const int t = r / a.group;  // row0 is a token's first row
+    const int64_t tok = quot(job.row0, a.group) + t;
+    const int hq = job.head * a.group + r - t * a.group;
+    const float n = s.L > 0.f ? 1.f / s.L : (s.L == 0.f ? 0.f : s.L);
+    Pack<T, E> y;
+#pragma unroll
+    for (int k = 0; k < E; ++k) from_f(s.acc[k] * n, y.v[k]);
+    *reinterpret_cast<Pack<T, E>*>((T*)a.out + (tok * a.heads_q + hq) * D + lane * E) = y;
+    if (a.lse && lane == 0)
+        a.lse[tok * a.heads_q + hq] = s.L > 0.f ? (s.m + log2f(s.L)) * 0.69314718056f : s.m;
+}
 
 // NB: blocks of 8 query rows.
 template <int FMT, int D, int NB, typename T>
@@ -176,58 +279,127 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     const int self = blockIdx.x * kWarps + warp;
     WarpSmem<D>& ws = sm.w[warp];
     volatile int* abort = &sm.abort;
-    if (threadIdx.x == 0) sm.abort = 0;
+    if (threadIdx.x == 0) {
+        sm.abort = 0;
+        sm.beyond = 0;
+        sm.early.parts = 0;
+    }
+    if (lane == 0) {
+        sm.own[warp].parts = 0;
+        sm.outside[warp] = 0;
+    }
     if (lane < NS) mbar_init(&sm.full[warp][lane], 1);
     fence_mbar_init();
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
     grid_begin();
+    // (blocks are dispatched in order, and one that gives up has waited for a second)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *parts.status = 0;
 
-    // ---- the batch's steps: a run of entries a thread, prefix over the block
+    // ---- the batch's steps and items: a run of entries a thread, prefixes over the block
     const int run = (a.ns + kThreads - 1) / kThreads;
     {
-        int64_t mine = 0;
-        for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i)
-            mine += span_of(a, i).steps;
-        int64_t inc = mine;
+        int64_t steps = 0;
+        int items = 0, most = 0;
+        for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i) {
+            const Span s = span_of(a, i);
+            steps += s.steps;
+            items = min(items + (s.steps > 0 ? a.v.heads : 0), 1 << 20);
+            most = max(most, s.steps > 0 ? s.tiles : 0);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
+            const int64_t x = __shfl_up_sync(0xffffffffu, steps, o);
+            const int y = __shfl_up_sync(0xffffffffu, items, o);
+            if (lane >= o) {
+                steps += x;
+                items += y;
+            }
         }
-        if (lane == 31) sm.sums[warp] = inc;
+        if (lane == 31) {
+            sm.warp_steps[warp] = steps;
+            sm.warp_items[warp] = items;
+            sm.warp_most[warp] = most;
+        }
         __syncthreads();
-        for (int w = 0; w < warp; ++w) inc += sm.sums[w];
-        sm.pre[threadIdx.x + 1] = inc;
-        if (threadIdx.x == 0) sm.pre[0] = 0;
+        for (int w = 0; w < warp; ++w) {
+            steps += sm.warp_steps[w];
+            items += sm.warp_items[w];
+        }
+        sm.pre[threadIdx.x + 1] = steps;
+        sm.items[threadIdx.x + 1] = items;
+        if (threadIdx.x == 0) sm.pre[0] = sm.items[0] = 0;
         __syncthreads();
     }
     const int64_t total = sm.pre[kThreads];
-    const int busy = (int)min((int64_t)kWarps, max((int64_t)1, (total + gridDim.x - 1) / gridDim.x));
-    const int64_t units = min((int64_t)gridDim.x * busy, total);
-    const int64_t unit = (int64_t)blockIdx.x * busy + warp;
-    int64_t g0 = 0, g1 = 0;
-    if (warp < busy && unit < units) {
-        g0 = unit * total / units;
-        g1 = (unit + 1) * total / units;
-    }
-    if (lane == 0) parts.cut[self].parts = 0;
+    int most = 0;
+    for (int w = 0; w < kWarps; ++w) most = max(most, sm.warp_most[w]);
+    const bool by_item = sm.items[kThreads] <= (int)gridDim.x && most <= kItemTiles;
+    const int runs = (a.ns + run - 1) / run;
 
-    auto locate = [&](int64_t g, Place& p) {
-        int lo = 0, hi = kThreads;  // the run that holds step g
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (sm.pre[mid] <= g) lo = mid;
-            else hi = mid;
+    Place p = {};
+    int busy = 1;
+    int64_t g0 = 0, g1 = 0, units = 0, unit = 0, base = 0, rest = 0;
+    if (by_item) {
+        if ((int)blockIdx.x < sm.items[kThreads]) {
+            int lo = 0, hi = runs;  // the run that holds this block's item
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (sm.items[mid] <= (int)blockIdx.x) lo = mid;
+                else hi = mid;
+            }
+            int rem = blockIdx.x - sm.items[lo];
+            p.entry = lo * run;
+            while (true) {
+                p.s = span_of(a, p.entry);
+                const int n = p.s.steps > 0 ? a.v.heads : 0;
+                if (rem < n) break;
+                rem -= n;
+                ++p.entry;
+            }
+            p.head = rem;
+            busy = min(kWarps, p.s.tiles);
+            if (warp < busy) {
+                g0 = (unsigned)(warp * p.s.tiles) / (unsigned)busy;
+                g1 = (unsigned)((warp + 1) * p.s.tiles) / (unsigned)busy;
+                p.t = (int)g0;
+            }
         }
-        int64_t rem = g - sm.pre[lo];
-        int i = lo * run;
-        while (true) {
-            p.s = span_of(a, i);
-            if (rem < p.s.steps) break;
-            rem -= p.s.steps;
-            ++i;
+        unit = (int64_t)blockIdx.x * busy + warp;
+    } else {
+        busy = (int)min((int64_t)kWarps, quot(total + gridDim.x - 1, gridDim.x));
+        units = min((int64_t)gridDim.x * busy, total);
+        unit = (int64_t)blockIdx.x * busy + warp;
+        // the first `rest` units take base + 1 steps, the others base
+        base = quot(total, units);
+        rest = total - base * units;
+        if (warp < busy && unit < units) {
+            g0 = unit * base + min(unit, rest);
+            g1 = g0 + base + (unit < rest ? 1 : 0);
+            int lo = 0, hi = runs;  // the run that holds step g0
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (sm.pre[mid] <= g0) lo = mid;
+                else hi = mid;
+            }
+            int64_t rem = g0 - sm.pre[lo];
+            p.entry = lo * run;
+            while (true) {
+                p.s = span_of(a, p.entry);
+                if (rem < p.s.steps) break;
+                rem -= p.s.steps;
+                ++p.entry;
+            }
+            p.open(rem);
         }
-        p.entry = i;
-        p.open(rem);
+    }
+    // the unit that takes a step
+    auto owner = [&](int64_t step) {
+        const int64_t head = rest * (base + 1);
+        return step < head ? quot(step, base + 1) : rest + quot(step - head, base);
     };
     // On to the next step's place, over entries without steps.
     auto advance = [&](Place& p) {
@@ -243,7 +415,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     // ---- producer: tile loads NS - 1 ahead, page ids one further, scales into
     // shared memory one tile later: nothing waits for a lookup.  Lane j < 4 serves
     // half j & 1 of the tile (pages of 16 end inside it), K (j < 2) or V.
-    Place pp = {};
+    Place pp = p;
     int64_t gp = g0;
     uint32_t np = 0;  // tiles produced
     const int box = min(a.v.page, kTile), nbox = kTile / box;
@@ -287,11 +459,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         }
     };
 
-    Place p = {};
     bool ok = true;
     if (g0 < g1) {
-        locate(g0, pp);
-        p = pp;
         lookup();
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) produce();
@@ -481,7 +650,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         }
         if (!ok) break;
         const bool begins = t_begin == 0, ends = t_end == p.s.tiles;
+        // where a part goes: units first .. last share the item
+        const int64_t block0 = (int64_t)blockIdx.x * busy;
+        int64_t first = block0, last = block0 + busy - 1;
+        if (!by_item && !(begins && ends)) {
+            const int64_t start = g - t_begin;
+            first = begins ? unit : owner(start);
+            last = ends ? unit : owner(start + p.s.tiles - 1);
+        }
+        const bool inside = first >= block0 && last < block0 + busy;
+        const bool in_ring = inside && g + (t_end - t_begin) == g1;  // nothing more comes into the ring
         const int64_t slot = 2 * (int64_t)self + (begins ? 1 : 0);
+        float2* part_ml = in_ring ? sm.ml[warp] : parts.ml + slot * kRows;
+        float* part_o = in_ring ? reinterpret_cast<float*>(&ws) : parts.o + slot * kRows * D;
 #pragma unroll
         for (int u = 0; u < 2 * NB; ++u) {
 #pragma unroll
@@ -503,23 +684,26 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                 if (a.lse && r0 == 0)
                     a.lse[tok * a.heads_q + hq] = L[u] > 0.f ? (m[u] + log2f(L[u])) * 0.69314718056f : m[u];
             } else {
-                if (r0 == 0) parts.ml[slot * kRows + r] = make_float2(m[u], L[u]);
-                float* dst = parts.o + (slot * kRows + r) * D + 2 * r0;
+                if (r0 == 0) part_ml[r] = make_float2(m[u], L[u]);
+                float* dst = part_o + r * D + 2 * r0;
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch)
                     *reinterpret_cast<float2*>(dst + 16 * ch) =
                         make_float2(o[nb][ch][j] * R, o[nb][ch][2 + j] * R);
             }
         }
-        if (begins && !ends && lane == 0) {
-            const int64_t last = g + p.s.tiles - 1;  // the item's last step: its warp
-            Cut c;
-            c.parts = (int)(((last + 1) * units - 1) / total - unit + 1);
-            c.rows = nrows;
-            c.head = p.head;
-            c.per_block = busy;
-            c.row0 = e.c0 * a.group;
-            parts.cut[self] = c;
+        if (lane == 0 && !(begins && ends)) {
+            if (inside ? begins : warp == 0 && first < block0 && last < block0 + busy) {
+                Job job;
+                job.first = first;
+                job.parts = (int)(last - first + 1);
+                job.rows = nrows;
+                job.head = p.head;
+                job.row0 = e.c0 * a.group;
+                (inside ? sm.own[warp] : sm.early) = job;
+            }
+            if (inside && !in_ring) sm.outside[warp] = 1;
+            if (last >= block0 + busy && g + (t_end - t_begin) == g1 && warp == busy - 1) sm.beyond = 1;
         }
         g += t_end - t_begin;
         if (g < g1) {
@@ -534,96 +718,84 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         for (; nc < np; ++nc) mbar_wait(&sm.full[warp][nc % NS], (nc / NS) & 1, &none, kWaitNs);
     }
     __syncthreads();
-    if (threadIdx.x == 0) parts.block_status[blockIdx.x] = sm.abort ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 80 : 0;
-}
 
-// Joins the parts of the items that were cut: block u the item that begins in
-// warp u and does not end there.  8 warps share the rows, and the parts of a row.
-constexpr int kMergeWarps = 8;
-template <int D, typename T>
-__global__ __launch_bounds__(32 * kMergeWarps) void k_attn_merge(const Attn a, const Parts parts, int blocks) {
-    __shared__ float s_m[kMergeWarps], s_L[kMergeWarps];
-    __shared__ float s_o[kMergeWarps][D];
-    grid_begin();
-    const int u = blockIdx.x;
-    if (u == 0) {  // the call's status
-        int st = 0;
-        for (int i = threadIdx.x; i < blocks; i += 32 * kMergeWarps) st = min(st, parts.block_status[i]);
-        st = __syncthreads_or(st);
-        if (threadIdx.x == 0) *parts.status = st ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 80 : 0;
+    // ---- joining
+    if (threadIdx.x == 0 && sm.beyond) set_flag(&parts.flag[blockIdx.x], parts.nonce);
+    const Job job = sm.early;
+    if (warp == 0 && job.parts) {
+        const uint64_t t0 = globaltimer();
+        bool all;
+        do {
+            all = true;
+            for (int i = (int)quot(job.first, busy) + lane; i < (int)blockIdx.x; i += 32)
+                all &= get_flag(&parts.flag[i]) == parts.nonce;
+            all = __all_sync(0xffffffffu, all);
+        } while (!all && __all_sync(0xffffffffu, globaltimer() - t0 < kWaitNs));
+        if (!all) sm.abort = 1;
+        for (int i = (int)quot(job.first, busy) + lane; i < (int)blockIdx.x; i += 32) parts.flag[i] = 0;
     }
-    const Cut c = parts.cut[u];
-    if (c.parts == 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int E = D / 32;
-    // part i of the item: 2u + 1 first, then part 2v of the i-th busy warp v behind u
-    const int block = u / kWarps, first = u % kWarps;
-    auto slot = [&](int i) {
-        const int w = first + i, b = w / c.per_block;
-        return i == 0 ? 2 * (int64_t)u + 1 : 2 * ((int64_t)(block + b) * kWarps + w - b * c.per_block);
-    };
-    // per: warps that share a row
-    const int per = c.rows == 1 ? 8 : c.rows == 2 ? 4 : c.rows <= 4 ? 2 : 1;
-    for (int r0 = 0; r0 < c.rows; r0 += kMergeWarps / per) {
-        const int r = r0 + warp / per, sub = warp % per;
-        float m = -INFINITY, L = 0.f, acc[E];
-#pragma unroll
-        for (int k = 0; k < E; ++k) acc[k] = 0.f;
-        if (r < c.rows) {
-            for (int i = sub + lane * per; i < c.parts; i += 32 * per) m = fmaxf(m, parts.ml[slot(i) * kRows + r].x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-            for (int i = sub; i < c.parts; i += per) {
-                const int64_t pr = slot(i) * kRows + r;
-                const float2 ml = parts.ml[pr];
-                const float* src = parts.o + pr * D + lane * E;
-                float x[E];
-                if (E == 4) *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
-                else *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
-                const float w = ex2(ml.x - base);
-                L = fmaf(w, ml.y, L);
-#pragma unroll
-                for (int k = 0; k < E; ++k) acc[k] = fmaf(w, x[k], acc[k]);
-            }
+    // items within the block: a warp a row
+    uint32_t jobs = __ballot_sync(0xffffffffu, lane < busy && sm.own[lane % kWarps].parts > 0);
+    for (int at = 0; jobs; jobs &= jobs - 1) {
+        const int w0 = __ffs(jobs) - 1;
+        const Job& own = sm.own[w0];
+        const int n = own.parts, tail = w0 + n - 1;
+        const bool outside = sm.outside[tail];  // the last part, in the workspace
+        const int64_t far = (int64_t)2 * (blockIdx.x * kWarps + tail) * kRows;
+        for (int r = (warp + kWarps - at) % kWarps; r < own.rows; r += kWarps) {
+            const Sum<D> s = sum_parts<D>(
+                n, 0, 1, lane,
+                [&](int j) { return outside && j == n - 1 ? parts.ml[far + r] : sm.ml[w0 + j][r]; },
+                [&](int j) -> const float* {
+                    return outside && j == n - 1 ? parts.o + (far + r) * D
+                                                 : reinterpret_cast<const float*>(&sm.w[w0 + j]) + r * D;
+                });
+            write_row<D, T>(a, own, r, s, lane);
         }
-        if (per > 1) {
-            if (lane == 0) {
-                s_m[warp] = m;
-                s_L[warp] = L;
-            }
+        at = (at + own.rows) % kWarps;
+    }
+    if (job.parts) {
+        __syncthreads();  // the rings are free, the flags were there
+        struct alignas(16) Row {  // acc is read 16 bytes at a time
+            float acc[D], m, L;
+        };
+        static_assert(sizeof(Row) * kWarps <= sizeof(sm.w), "the ring holds the warps' sums");
+        Row* rows = reinterpret_cast<Row*>(sm.w);
+        const int b0 = (int)quot(job.first, busy), w0 = (int)(job.first - (int64_t)b0 * busy);
+        const int per = max(1, kWarps / job.rows);  // warps that share a row
+        for (int r0 = 0; r0 < job.rows && !sm.abort; r0 += kWarps / per) {
+            const int r = r0 + warp / per, sub = warp % per;
+            const bool mine = warp / per < kWarps / per && r < job.rows;
+            auto at = [&](int i) {  // part i of the row
+                const int v = w0 + i, b = (int)((unsigned)v / (unsigned)busy);
+                const int64_t w = (int64_t)(b0 + b) * kWarps + v - b * busy;
+                return (2 * w + (i == 0 ? 1 : 0)) * kRows + r;
+            };
+            Sum<D> s;
+            if (mine)
+                s = sum_parts<D>(
+                    job.parts, sub, per, lane, [&](int i) { return __ldcg(&parts.ml[at(i)]); },
+                    [&](int i) -> const float* { return parts.o + at(i) * D; });
+            if (per > 1) {
+                if (mine) {
+                    if (lane == 0) {
+                        rows[warp].m = s.m;
+                        rows[warp].L = s.L;
+                    }
 #pragma unroll
-            for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = acc[k];
-            __syncthreads();
-            if (sub == 0 && r < c.rows) {
-                float top = -INFINITY;
-                for (int w = warp; w < warp + per; ++w) top = fmaxf(top, s_m[w]);
-                const float base = top == -INFINITY ? 0.f : top;
-                L = 0.f;
-#pragma unroll
-                for (int k = 0; k < E; ++k) acc[k] = 0.f;
-                for (int w = warp; w < warp + per; ++w) {
-                    const float f = ex2(s_m[w] - base);
-                    L = fmaf(f, s_L[w], L);
-#pragma unroll
-                    for (int k = 0; k < E; ++k) acc[k] = fmaf(f, s_o[w][lane * E + k], acc[k]);
+                    for (int k = 0; k < D / 32; ++k) rows[warp].acc[lane * (D / 32) + k] = s.acc[k];
                 }
-                m = top;
+                __syncthreads();
+                if (mine && sub == 0)
+                    s = sum_parts<D>(
+                        per, 0, 1, lane, [&](int i) { return make_float2(rows[warp + i].m, rows[warp + i].L); },
+                        [&](int i) -> const float* { return rows[warp + i].acc; });
+                __syncthreads();
             }
-        }
-        if (sub == 0 && r < c.rows) {
-            const int64_t ri = c.row0 + r, tok = ri / a.group;
-            const int hq = c.head * a.group + (int)(ri % a.group);
-            const float n = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-            Pack<T, E> y;
-#pragma unroll
-            for (int k = 0; k < E; ++k) from_f(acc[k] * n, y.v[k]);
-            *reinterpret_cast<Pack<T, E>*>((T*)a.out + (tok * a.heads_q + hq) * D + lane * E) = y;
-            if (a.lse && lane == 0)
-                a.lse[tok * a.heads_q + hq] = L > 0.f ? (m + log2f(L)) * 0.69314718056f : m;
+            if (mine && sub == 0) write_row<D, T>(a, job, r, s, lane);
         }
     }
+    if (threadIdx.x == 0 && sm.abort) *parts.status = TQ_ERR_DEVICE_TIMEOUT * 1000 - 80;
 }
 
 constexpr int kMaxBlocks = 148;  // the workspace's size
@@ -649,14 +821,12 @@ bool any_many(const tq_kv8_t* c, int max_q, int heads_q) {
 template <int D>
 Parts carve(void* ws, int64_t blocks, size_t* bytes) {
     const int64_t units = blocks * kWarps;
-    Parts p;
+    Parts p = {};
     char* at = (char*)ws;
     p.status = (int*)at;
     at += 256;
-    p.block_status = (int*)at;
-    at += align256(blocks * 4);
-    p.cut = (Cut*)at;
-    at += align256(units * sizeof(Cut));
+    p.flag = (uint64_t*)at;
+    at += align256(blocks * 8);
     p.ml = (float2*)at;
     at += align256(2 * units * kRows * sizeof(float2));
     p.o = (float*)at;
@@ -671,9 +841,7 @@ int launch(const Attn& a, const CUtensorMap& km, const CUtensorMap& vm, const Pa
     constexpr int smem = (int)sizeof(Smem<D>) + 1024;
     static_assert(smem <= 232448, "shared memory of a block");
     int rc = allow_smem<k_attn_rows<FMT, D, NB, T>>(smem);
-    if (!rc) rc = launch_behind(k_attn_rows<FMT, D, NB, T>, dim3(blocks), kThreads, smem, s, a, km, vm, p);
-    if (!rc) rc = launch_behind(k_attn_merge<D, T>, dim3(blocks * kWarps), 32 * kMergeWarps, 0, s, a, p, blocks);
-    return rc;
+    return rc ? rc : launch_behind(k_attn_rows<FMT, D, NB, T>, dim3(blocks), kThreads, smem, s, a, km, vm, p);
 }
 
 template <int FMT, int D, typename T>
@@ -691,6 +859,15 @@ int dispatch(const tq_kv8_t* c, const Attn& a, const CUtensorMap& km, const CUte
                                   : launch_rows<TQ_KV_I8, D, __half>(a, km, vm, p, blocks, rows, s);
     return q_dtype == TQ_BF16 ? launch_rows<TQ_KV_E4M3, D, __nv_bfloat16>(a, km, vm, p, blocks, rows, s)
                               : launch_rows<TQ_KV_E4M3, D, __half>(a, km, vm, p, blocks, rows, s);
+}
+
+// A value that no earlier call has left in a workspace.
+uint64_t new_nonce() {
+    static std::atomic<uint64_t> next{
+        (uint64_t)std::chrono::system_clock::now().time_since_epoch().count() * 0xD1342543DE82EF95ull ^
+        (uint64_t)(uintptr_t)&next};
+    const uint64_t x = next.fetch_add(0x9E3779B97F4A7C15ull);  // an odd step: all values in turn
+    return x ? x : next.fetch_add(0x9E3779B97F4A7C15ull);      // (0: a flag that was taken back)
 }
 
 Parts carve_for(const tq_kv8_t* c, void* ws, int64_t blocks, size_t* bytes) {
@@ -763,7 +940,8 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
         if (!rc) rc = kv8::code_map(&vm, (const char*)c->d_v + layer * kv8::layer_bytes(c), c->d, a.rows, box);
         if (rc) return rc;
         const int blocks = (int)kv8::blocks_for(c, ns);
-        const kv8::Parts p = kv8::carve_for(c, d_ws, blocks, &at);
+        kv8::Parts p = kv8::carve_for(c, d_ws, blocks, &at);
+        p.nonce = kv8::new_nonce();
         rc = c->d == 128 ? kv8::dispatch<128>(c, a, km, vm, p, blocks, a.few, q_dtype, s)
                          : kv8::dispatch<64>(c, a, km, vm, p, blocks, a.few, q_dtype, s);
         if (rc) return rc;

@@ -27,11 +27,11 @@ struct Attn {
                // kernel, the others on the prompt kernel (0: all of them)
 };
 
-// An item that its warp (or CTA) begins and others go on with: who joins what.
+// An item that its CTA begins and others go on with: who joins what.
 struct Cut {
-    int parts;       // streams that share the item which begins here; 0: none
+    int parts;       // CTAs that share the item which begins here; 0: none
     int rows, head;  // its rows and KV head
-    int per_block;   // few-rows kernel: busy warps of a block
+    int pad;
     int64_t row0;    // its first row of the entry's (token x group) rows, from token 0
 };
 

@@ -446,7 +446,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     c.parts = (int)(((last + 1) * units - 1) / total) - unit + 1;
                     c.rows = (int)min((int64_t)kPRows, rows - (int64_t)it.part * kPRows);
                     c.head = it.head;
-                    c.per_block = 1;
+                    c.pad = 0;
                     c.row0 = e.c0 * a.group + (int64_t)it.part * kPRows;
                     parts.cut[unit] = c;
                 }
