@@ -55,6 +55,15 @@ struct AppendArgs {
     int rope;
 };
 
+constexpr float kLargest = 1.7014118e38f;  // 2^127
+
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // NI items of 2 VEC elements a thread; VEC = 8 (16-byte accesses) or 1.
 template <typename T, int FMT, int VEC, int NI>
 __global__ __launch_bounds__(256) void k_append(const AppendArgs a,
@@ -140,12 +149,19 @@ __global__ __launch_bounds__(256) void k_append(const AppendArgs a,
                 }
             }
 #pragma unroll
+            for (int e = 0; e < 2 * VEC; ++e) top = max_nan(top, fabsf(val[i][e]));
+        }
+    }
+    if (!(top <= kLargest)) {  // NaN: 0; up to 2^127, so that scale x code stays finite
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if ((int)(threadIdx.x + i * blockDim.x) >= n) continue;
+#pragma unroll
             for (int e = 0; e < 2 * VEC; ++e) {
-                float y = val[i][e];
-                // NaN: 0; up to 2^127, so that scale x code stays finite
-                y = y == y ? fminf(fmaxf(y, -1.7014118e38f), 1.7014118e38f) : 0.f;
-                val[i][e] = y;
-                top = fmaxf(top, fabsf(y));
+                const float y = val[i][e];
+                val[i][e] = y == y ? fminf(fmaxf(y, -kLargest), kLargest) : 0.f;
+                top = fmaxf(top, fabsf(val[i][e]));
             }
         }
     }
@@ -156,6 +172,15 @@ __global__ __launch_bounds__(256) void k_append(const AppendArgs a,
     for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, s_red[w]);
     const float s = fmaxf(s_old, __fdiv_rn(top, code_max<FMT>()));
     if (threadIdx.x == 0) a.scale[kv][ph] = s;
+    // (below fp32's normal range a reciprocal may overflow: all times 2^64)
+    const float up = s < 1.17549435e-38f ? 18446744073709551616.f : 1.f;
+    const float inv = s > 0.f ? __frcp_rn(s * up) : 0.f;
+    if (up != 1.f) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int e = 0; e < 2 * VEC; ++e) val[i][e] *= up;
+    }
 
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -167,26 +192,41 @@ __global__ __launch_bounds__(256) void k_append(const AppendArgs a,
             const int o2 = pair ? m * VEC + half : o1 + VEC;
             uint8_t* cr = codes + (row0 + row) * v.d;
             if (VEC == 8) {
-                uint32_t w[4] = {0, 0, 0, 0};
+                uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 2 * VEC; ++e) w[e / 4] |= encode<FMT>(val[i][e], s) << (8 * (e & 3));
+                for (int e = 0; e < 4; ++e)
+                    w[e] = encode4<FMT>(val[i][4 * e % (2 * VEC)], val[i][(4 * e + 1) % (2 * VEC)],
+                                        val[i][(4 * e + 2) % (2 * VEC)], val[i][(4 * e + 3) % (2 * VEC)], inv);
                 *reinterpret_cast<uint2*>(cr + o1) = make_uint2(w[0], w[1]);
                 *reinterpret_cast<uint2*>(cr + o2) = make_uint2(w[2], w[3]);
             } else {
-                cr[o1] = (uint8_t)encode<FMT>(val[i][0], s);
-                cr[o2] = (uint8_t)encode<FMT>(val[i][1], s);
+                const uint32_t w = encode4<FMT>(val[i][0], val[i][1], 0.f, 0.f, inv);
+                cr[o1] = (uint8_t)w;
+                cr[o2] = (uint8_t)(w >> 8);
             }
         }
     }
     if (row0 > 0 && s > s_old) {  // the page's old rows, for the new scale
-        uint32_t* w = reinterpret_cast<uint32_t*>(codes);
-        for (int i = threadIdx.x; i < row0 * v.d / 4; i += blockDim.x) {
-            const uint32_t c = w[i];
-            uint32_t r = 0;
+        const float f = s_old * up * inv;
+        uint4* w = reinterpret_cast<uint4*>(codes);
+        const int nw = row0 * v.d / 16;
+        for (int i0 = threadIdx.x; i0 < nw; i0 += 4 * blockDim.x) {
+            uint4 c[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                r |= encode<FMT>(decode<FMT>((c >> (8 * e)) & 0xFFu) * s_old, s) << (8 * e);
-            w[i] = r;
+                if (i0 + e * (int)blockDim.x < nw) c[e] = w[i0 + e * blockDim.x];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (i0 + e * (int)blockDim.x >= nw) continue;
+                uint32_t y[4] = {c[e].x, c[e].y, c[e].z, c[e].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float x[4];
+                    decode4<FMT>(y[k], x);
+                    y[k] = encode4<FMT>(x[0], x[1], x[2], x[3], f);
+                }
+                w[i0 + e * blockDim.x] = make_uint4(y[0], y[1], y[2], y[3]);
+            }
         }
     }
 }
@@ -206,7 +246,6 @@ int append_fmt(const AppendArgs& a, const tq_rope_params_t& r, int ns, int max_n
     const int rows = max_new < a.v.page ? max_new : a.v.page;
     if (wide) {
         const int items = rows * a.v.d / 16;
-        if (items <= 64) return append_go<T, FMT, 8, 1>(a, r, ns, 64, s);
         if (items <= 128) return append_go<T, FMT, 8, 1>(a, r, ns, 128, s);
         if (items <= 256) return append_go<T, FMT, 8, 1>(a, r, ns, 256, s);
         if (items <= 512) return append_go<T, FMT, 8, 2>(a, r, ns, 256, s);
@@ -231,64 +270,83 @@ int append_type(const tq_kv8_t* c, const AppendArgs& a, const tq_rope_params_t& 
 // ---- read -------------------------------------------------------------------
 
 constexpr int kReadThreads = 256;
+constexpr int kReadItems = 4;  // of 16 codes, a thread
 
-// A block reads `tokens` tokens of one slot, all heads, K and V: 16 codes a step.
+// A block reads `tokens` tokens of one slot, all heads, K or V: 16 codes an item.
+// The lookups of a thread's items, then their codes, are on their way together.
 template <typename T, int FMT>
-__global__ __launch_bounds__(kReadThreads) void k_read(View v, const int32_t* slots,
-                                                       const int32_t* begin,
-                                                       const int32_t* cu, int bps,
-                                                       int tokens, int64_t total,
-                                                       const uint8_t* kc,
-                                                       const uint8_t* vc,
-                                                       const float* ks,
-                                                       const float* vs, T* out_k,
-                                                       T* out_v) {
+__global__ __launch_bounds__(kReadThreads) void k_read(View v, const int32_t* slots, const int32_t* begin,
+                                                       const int32_t* cu, int bps, int tokens, int64_t total,
+                                                       const uint8_t* kc, const uint8_t* vc, const float* ks,
+                                                       const float* vs, T* out_k, T* out_v) {
     grid_begin();
     const int seq = blockIdx.x / bps, blk = blockIdx.x - seq * bps;
     const int slot = slot_of(v, slots, seq);
-    const int64_t c0 = max(cu[seq], 0);
-    const int count = (int)(min((int64_t)cu[seq + 1], total) - c0);
-    const int t0 = blk * tokens, nt = min(tokens, count - t0);
-    if (nt <= 0) return;
+    const int64_t c0 = max(cu[seq], 0), c1 = min((int64_t)cu[seq + 1], total);
+    const int64_t b = (int64_t)begin[seq] + (int64_t)blk * tokens;
     const int len = slot >= 0 ? length_of(v, slot) : 0;
-    const int64_t b = (int64_t)begin[seq] + t0;
-    const int chunks = v.d / 16, per = v.heads * chunks;
+    const int nt = (int)min((int64_t)tokens, c1 - c0 - (int64_t)blk * tokens);
+    if (nt <= 0) return;
+    const int chunks = v.d / 16, per = v.heads * chunks, n = nt * per;
     const bool is_v = blockIdx.y != 0;
     T* out = is_v ? out_v : out_k;
     if (!out) return;
     const uint8_t* codes = is_v ? vc : kc;
-    const float* scale = is_v ? vs : ks;
-    for (int i = threadIdx.x; i < nt * per; i += kReadThreads) {
-        const int t = i / per, hc = i - t * per, h = hc / chunks, ch = hc - h * chunks;
-        const int64_t pos = b + t;
-        int pid = -1;
-        if (pos >= 0 && pos < len) pid = page_of(v, slot, (int)(pos >> v.page_log2));
-        Pack<T, 8> o[2];
-        uint4 w = make_uint4(0, 0, 0, 0);
-        float s = 0.f;
-        if (pid >= 0) {
-            const int64_t ph = (int64_t)pid * v.heads + h;
-            w = *reinterpret_cast<const uint4*>(
-                codes + ((ph << v.page_log2) + (pos & (v.page - 1))) * v.d + 16 * ch);
-            s = scale[ph];
-        }
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    const float* scales = is_v ? vs : ks;
+    // (items of a block are neighbours in the output: token, head, chunk)
+    Pack<T, 8>* dst = reinterpret_cast<Pack<T, 8>*>(out + (c0 + (int64_t)blk * tokens) * v.heads * v.d);
+    for (int i0 = threadIdx.x; i0 < n; i0 += kReadItems * kReadThreads) {
+        int pid[kReadItems];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            from_f(pid >= 0 ? s * decode<FMT>((ww[e / 4] >> (8 * (e & 3))) & 0xFFu) : 0.f,
-                   o[e / 8].v[e % 8]);
-        Pack<T, 8>* dst = reinterpret_cast<Pack<T, 8>*>(out + ((c0 + t0 + t) * v.heads + h) * v.d + 16 * ch);
-        dst[0] = o[0];
-        dst[1] = o[1];
+        for (int e = 0; e < kReadItems; ++e) {
+            const int i = i0 + e * kReadThreads;
+            pid[e] = -1;
+            if (i < n) {
+                const int64_t pos = b + i / per;
+                if (pos >= 0 && pos < len) pid[e] = page_of(v, slot, (int)(pos >> v.page_log2));
+            }
+        }
+        uint4 w[kReadItems];
+        float s[kReadItems];
+#pragma unroll
+        for (int e = 0; e < kReadItems; ++e) {
+            const int i = i0 + e * kReadThreads;
+            w[e] = make_uint4(0, 0, 0, 0);
+            s[e] = 0.f;
+            if (pid[e] >= 0) {
+                const int t = i / per, hc = i - t * per, h = hc / chunks, ch = hc - h * chunks;
+                const int64_t ph = (int64_t)pid[e] * v.heads + h;
+                w[e] = *reinterpret_cast<const uint4*>(
+                    codes + ((ph << v.page_log2) + ((b + t) & (v.page - 1))) * v.d + 16 * ch);
+                s[e] = scales[ph];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kReadItems; ++e) {
+            const int i = i0 + e * kReadThreads;
+            if (i >= n) continue;
+            const uint32_t ww[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+            Pack<T, 8> o[2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float x[4];
+                decode4<FMT>(ww[k], x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) from_f(s[e] * x[j], o[k / 2].v[4 * (k & 1) + j]);
+            }
+            dst[2 * (int64_t)i] = o[0];
+            dst[2 * (int64_t)i + 1] = o[1];
+        }
     }
 }
 
 template <typename T>
 int read_type(const tq_kv8_t* c, int layer, int ns, const int32_t* slots, const int32_t* begin,
               const int32_t* cu, int64_t total, int max_new, void* k, void* v, cudaStream_t s) {
-    // about four steps a thread
+    // a batch of items a thread, or fewer tokens a block where that leaves SMs idle
     const int per = c->heads * c->d / 16;
-    int tokens = 4 * kReadThreads / per;
+    int64_t tokens = kReadItems * kReadThreads / per, fill = (int64_t)ns * max_new / (148 * 2);
+    if (tokens > fill) tokens = fill;
     tokens = tokens < 1 ? 1 : (tokens > max_new ? max_new : tokens);
     const int64_t bps = (max_new + tokens - 1) / tokens;
     if (bps * ns > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
@@ -298,7 +356,7 @@ int read_type(const tq_kv8_t* c, int layer, int ns, const int32_t* slots, const 
     const float* ks = c->d_kscale + layer * layer_scales(c);
     const float* vs = c->d_vscale + layer * layer_scales(c);
     return launch_behind(c->format == TQ_KV_I8 ? k_read<T, TQ_KV_I8> : k_read<T, TQ_KV_E4M3>, grid,
-                         kReadThreads, 0, s, view(c), slots, begin, cu, (int)bps, tokens, total, kc, vc,
+                         kReadThreads, 0, s, view(c), slots, begin, cu, (int)bps, (int)tokens, total, kc, vc,
                          ks, vs, (T*)k, (T*)v);
 }
 

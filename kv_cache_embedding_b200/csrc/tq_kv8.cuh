@@ -99,17 +99,33 @@ __device__ __forceinline__ void codes_to_half_02(uint32_t w, uint32_t& b02, uint
 template <int FMT>
 __host__ __device__ constexpr float code_max() { return FMT == TQ_KV_I8 ? 127.f : 448.f; }
 
-// x / s to the nearest code (ties to even), saturating; 0 for s = 0.
+// The nearest codes of four quotients x / s (ties to even): x times the fp32
+// reciprocal, off by 2^-23 of itself, so a code differs from the exact quotient's
+// only where that lies as close to the middle between two codes.  |x| <= s
+// code_max, so that nothing saturates.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode(float x, float s) {
-    const float v = s > 0.f ? __fdiv_rn(x, s) : 0.f;
-    if (FMT == TQ_KV_I8) return (uint32_t)(__float2int_rn(fminf(fmaxf(v, -127.f), 127.f))) & 0xFFu;
-    return (uint32_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float inv) {
+    if (FMT == TQ_KV_I8) {
+        // behind 1.5 2^23 the last bits of a sum are the integer, rounded by the addition
+        const uint32_t a = __float_as_uint(fmaf(x0, inv, 12582912.f)), b = __float_as_uint(fmaf(x1, inv, 12582912.f));
+        const uint32_t c = __float_as_uint(fmaf(x2, inv, 12582912.f)), d = __float_as_uint(fmaf(x3, inv, 12582912.f));
+        return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+    }
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 * inv, x1 * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2 * inv, x3 * inv), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
 }
+__device__ __forceinline__ float2 half2_to_f(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+// Four codes' values, exact.
 template <int FMT>
-__device__ __forceinline__ float decode(uint32_t byte) {
-    if (FMT == TQ_KV_I8) return (float)(int8_t)byte;
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
+__device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
+    uint32_t lo, hi;
+    codes_to_half<FMT>(w, lo, hi);
+    const float2 a = half2_to_f(lo), b = half2_to_f(hi);
+    x[0] = a.x;
+    x[1] = a.y;
+    x[2] = b.x;
+    x[3] = b.y;
 }
 
 __device__ __forceinline__ float to_f(float x) { return x; }

@@ -36,66 +36,88 @@ struct alignas(sizeof(T) * VEC) Pack {
     T v[VEC];
 };
 
-// VEC: elements per access (16 bytes, or 1).  An item is two runs of VEC
-// elements for the half layout's pairs (i, i + rot/2), one run otherwise; with
-// VEC = 1 an interleaved pair is two runs of one.
-template <typename T, int VEC>
+// VEC: elements per access (16 bytes, or 1).  SPLIT: an item is two runs of VEC
+// elements, the half layout's pairs (i, i + rot/2) or with VEC = 1 an interleaved
+// pair; otherwise one run.  A thread loads a batch of items before it waits for
+// the angles, so the data are on their way meanwhile (and for many tokens 64 bytes
+// a thread are in flight).
+template <typename T, int VEC, bool SPLIT>
 __global__ __launch_bounds__(kRT) void k_rope(const __grid_constant__ tq_rope_params_t r, int64_t T_,
-                                              int heads, const T* x, int64_t x_ts,
-                                              int64_t x_hs, const int64_t* pos, T* out,
-                                              int64_t out_ts, int64_t out_hs, int transpose,
-                                              int tokens, int in_place) {
+                                              int heads, const T* x, int64_t x_ts, int64_t x_hs,
+                                              const int64_t* pos, T* out, int64_t out_ts,
+                                              int64_t out_hs, int transpose, int tokens, int in_place) {
     extern __shared__ float2 s_cs[];  // [tokens][rot/2]: a cos, a sin
     grid_begin();
     using P = Pack<T, VEC>;
+    constexpr int N = SPLIT ? 2 : 4;  // items of a batch
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int nt = (int)min((int64_t)tokens, T_ - t0);
     const int half = r.rot / 2;
-    for (int i = threadIdx.x; i < nt * half; i += kRT) {
-        const int t = i / half, m = i - t * half;
-        float c, s;
-        rope_angle(r.turns[m], pos[t0 + t], c, s);
-        s_cs[i] = make_float2(c * r.amplitude, (transpose ? -s : s) * r.amplitude);
-    }
-    __syncthreads();
-    const bool split = r.layout == TQ_ROPE_HALF || VEC == 1;  // items of two runs
-    const int turned = split ? half / VEC : r.rot / VEC;
+    const int turned = SPLIT ? half / VEC : r.rot / VEC;
     const int items = turned + (in_place ? 0 : (r.d - r.rot) / VEC);
-    const int per = heads * items;
-    for (int i = threadIdx.x; i < nt * per; i += kRT) {
-        const int t = i / per, hi = i - t * per;
-        const int h = hi / items, it = hi - h * items;
-        const T* xr = x + (t0 + t) * x_ts + h * x_hs;
-        T* orow = out + (t0 + t) * out_ts + h * out_hs;
-        const float2* cs = s_cs + t * half;
-        if (it >= turned) {
-            const int o = r.rot + (it - turned) * VEC;
-            *reinterpret_cast<P*>(orow + o) = *reinterpret_cast<const P*>(xr + o);
-        } else if (split) {
-            const int m = it * VEC;
-            const int o1 = r.layout == TQ_ROPE_HALF ? m : 2 * m;
-            const int o2 = r.layout == TQ_ROPE_HALF ? m + half : 2 * m + 1;
-            P a = *reinterpret_cast<const P*>(xr + o1);
-            P b = *reinterpret_cast<const P*>(xr + o2);
+    const int per = heads * items, n = nt * per;
+    int64_t p0 = 0;
+    if ((int)threadIdx.x < nt * half) p0 = pos[t0 + threadIdx.x / half];
+    for (int i0 = threadIdx.x, first = 1; first || i0 - (int)threadIdx.x < n; i0 += N * kRT, first = 0) {
+        P a[N], b[N];
+        int64_t at[N];
+        int o1[N], o2[N], m[N], tok[N];  // m: first pair of a turned item, -1: copied
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float x1 = to_f(a.v[e]), x2 = to_f(b.v[e]);
-                const float2 w = cs[m + e];
-                from_f(x1 * w.x - x2 * w.y, a.v[e]);
-                from_f(x2 * w.x + x1 * w.y, b.v[e]);
+        for (int e = 0; e < N; ++e) {
+            const int i = i0 + e * kRT;
+            if (i >= n) continue;
+            const int t = i / per, hi = i - t * per, h = hi / items, it = hi - h * items;
+            const T* xr = x + (t0 + t) * x_ts + h * x_hs;
+            at[e] = (t0 + t) * out_ts + h * out_hs;
+            tok[e] = t;
+            if (it >= turned) {
+                m[e] = -1;
+                o1[e] = r.rot + (it - turned) * VEC;
+            } else if (SPLIT) {
+                m[e] = it * VEC;
+                o1[e] = r.layout == TQ_ROPE_HALF ? m[e] : 2 * m[e];
+                o2[e] = r.layout == TQ_ROPE_HALF ? m[e] + half : 2 * m[e] + 1;
+                b[e] = *reinterpret_cast<const P*>(xr + o2[e]);
+            } else {
+                o1[e] = it * VEC;
+                m[e] = it * VEC / 2;
             }
-            *reinterpret_cast<P*>(orow + o1) = a;
-            *reinterpret_cast<P*>(orow + o2) = b;
-        } else {
-            P a = *reinterpret_cast<const P*>(xr + it * VEC);
+            a[e] = *reinterpret_cast<const P*>(xr + o1[e]);
+        }
+        if (first) {
+            for (int i = threadIdx.x; i < nt * half; i += kRT) {
+                const int t = i / half, k = i - t * half;
+                float c, s;
+                rope_angle(r.turns[k], i == (int)threadIdx.x ? p0 : pos[t0 + t], c, s);
+                s_cs[i] = make_float2(c * r.amplitude, (transpose ? -s : s) * r.amplitude);
+            }
+            __syncthreads();
+        }
 #pragma unroll
-            for (int e = 0; e + 1 < VEC; e += 2) {
-                const float x1 = to_f(a.v[e]), x2 = to_f(a.v[e + 1]);
-                const float2 w = cs[(it * VEC + e) / 2];
-                from_f(x1 * w.x - x2 * w.y, a.v[e]);
-                from_f(x2 * w.x + x1 * w.y, a.v[e + 1]);
+        for (int e = 0; e < N; ++e) {
+            if (i0 + e * kRT >= n) continue;
+            if (m[e] >= 0) {
+                const float2* cs = s_cs + tok[e] * half + m[e];
+                if (SPLIT) {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) {
+                        const float x1 = to_f(a[e].v[k]), x2 = to_f(b[e].v[k]);
+                        const float2 w = cs[k];
+                        from_f(x1 * w.x - x2 * w.y, a[e].v[k]);
+                        from_f(x2 * w.x + x1 * w.y, b[e].v[k]);
+                    }
+                    *reinterpret_cast<P*>(out + at[e] + o2[e]) = b[e];
+                } else {
+#pragma unroll
+                    for (int k = 0; k + 1 < VEC; k += 2) {
+                        const float x1 = to_f(a[e].v[k]), x2 = to_f(a[e].v[k + 1]);
+                        const float2 w = cs[k / 2];
+                        from_f(x1 * w.x - x2 * w.y, a[e].v[k]);
+                        from_f(x2 * w.x + x1 * w.y, a[e].v[k + 1]);
+                    }
+                }
             }
-            *reinterpret_cast<P*>(orow + it * VEC) = a;
+            *reinterpret_cast<P*>(out + at[e] + o1[e]) = a[e];
         }
     }
 }
@@ -116,9 +138,10 @@ int launch(const tq_rope_params_t& r, int64_t T_, int heads, const void* x, int6
     const int64_t blocks = (T_ + tokens - 1) / tokens;
     if (blocks > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
     const size_t smem = (size_t)tokens * (r.rot / 2) * sizeof(float2);
-    return launch_behind(wide ? k_rope<T, V> : k_rope<T, 1>, dim3((unsigned)blocks), kRT, smem, s, r, T_,
-                         heads, (const T*)x, x_ts, x_hs, pos, (T*)out, out_ts, out_hs, transpose, tokens,
-                         in_place);
+    auto kernel = !wide ? k_rope<T, 1, true>
+                  : r.layout == TQ_ROPE_HALF ? k_rope<T, V, true> : k_rope<T, V, false>;
+    return launch_behind(kernel, dim3((unsigned)blocks), kRT, smem, s, r, T_, heads, (const T*)x, x_ts, x_hs,
+                         pos, (T*)out, out_ts, out_hs, transpose, tokens, in_place);
 }
 
 }  // namespace
