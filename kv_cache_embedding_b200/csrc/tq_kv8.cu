@@ -5,11 +5,11 @@
 //   code = rnd(x / s),         old codes: rnd(code s0 / s) where s > s0,
 // keys turned to their positions first (fp32, not rounded in between).
 //
-// A block owns one (slot, page, head) of K or V, so the page's maximum is a
-// block reduction and nothing is written twice: its new rows are loaded once
-// into registers (16 elements an item), turned, reduced, rounded and stored;
-// the page's old rows are touched only when the scale grows.  Bound by HBM for
-// prompts, by the chain length -> table -> scale for single tokens.
+// A block owns whole (slot, page, head)s of K or V, so the page's maximum is a
+// block reduction and nothing is written twice: new rows are loaded once into
+// registers, turned, reduced, rounded and stored; the page's old rows are touched
+// only when the scale grows.  Bound by issue slots and HBM for prompts, by the
+// chain length -> table -> scale for single tokens.
 #include "tq_kv8.cuh"
 #include "tq_rope.cuh"
 
@@ -47,6 +47,7 @@ struct AppendArgs {
     const int32_t* slots;
     const int32_t* cu;
     int ppb;  // pages a slot's new tokens can touch
+    int hb;   // heads a block
     int64_t total;
     const void *x[2];
     int64_t x_ts, x_hs;
@@ -57,28 +58,31 @@ struct AppendArgs {
 
 constexpr float kLargest = 1.7014118e38f;  // 2^127
 
-// The larger one, NaN if either is.
+// The larger one of a and |b|, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 
-// NI items of 2 VEC elements a thread; VEC = 8 (16-byte accesses) or 1.
-template <typename T, int FMT, int VEC, int NI>
-__global__ __launch_bounds__(256) void k_append(const AppendArgs a,
-                                                const __grid_constant__ tq_rope_params_t rope) {
-    __shared__ float s_red[8];
+// A block writes `hb` heads of one page, one after another: an item of a thread
+// (two runs of VEC coordinates of a row, half the turned or the other part apart)
+// is the same in every head, so its angles are formed once, and the next head's
+// rows are on their way while this one's are rounded.  VEC = 8 (16-byte accesses)
+// or 1; NI items a thread; ROPE: 0 none, 1 half layout, 2 interleaved.
+template <typename T, int FMT, int VEC, int NI, int ROPE>
+__global__ __launch_bounds__(VEC == 8 ? 1024 : 256) void k_append(
+    const AppendArgs a, const __grid_constant__ tq_rope_params_t rope) {
+    __shared__ uint32_t s_red[2][32];
     grid_begin();
     const View& v = a.v;
     const int seq = blockIdx.x / a.ppb, pj = blockIdx.x - seq * a.ppb;
-    const int h = blockIdx.y, kv = blockIdx.z;
+    const int kv = blockIdx.z;
     const int slot = slot_of(v, a.slots, seq);
-    if (slot < 0) return;
     const int64_t c0 = max(a.cu[seq], 0);
     const int count = (int)(min((int64_t)a.cu[seq + 1], a.total) - c0);
+    if (slot < 0 || count <= 0) return;
     const int len = length_of(v, slot);
-    if (count <= 0) return;
     // tokens before the slot's first position have no place
     const int start = max(len - count, 0), skip = max(count - len, 0);
     const int page0 = start >> v.page_log2;
@@ -88,155 +92,189 @@ __global__ __launch_bounds__(256) void k_append(const AppendArgs a,
     const int pid = page_of(v, slot, page0 + pj);
     if (pid < 0) return;
     const int row0 = lo_pos & (v.page - 1), rows = hi_pos - lo_pos;
-    const int64_t ph = (int64_t)pid * v.heads + h;
-    uint8_t* codes = a.codes[kv] + (ph << v.page_log2) * v.d;
-    const T* x = (const T*)a.x[kv] + (c0 + skip + lo_pos - start) * a.x_ts + h * a.x_hs;
-    const float s_old = row0 > 0 ? a.scale[kv][ph] : 0.f;
-    const bool turn = kv == 0 && a.rope;
+    const int h0 = blockIdx.y * a.hb, h1 = min(v.heads, h0 + a.hb);
+    const int64_t ph0 = (int64_t)pid * v.heads;
+    const T* x = (const T*)a.x[kv] + (c0 + skip + lo_pos - start) * a.x_ts + h0 * a.x_hs;
+    const bool turn = ROPE && kv == 0;
 
-    const int per = v.d / (2 * VEC);  // items of a row
-    const int n = rows * per;
-    const int rot = turn ? rope.rot : 0, half = rot / 2;
-    const bool halves = turn && rope.layout == TQ_ROPE_HALF;
-    float val[NI][2 * VEC];
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int it = threadIdx.x + i * blockDim.x;
-        if (it < n) {
-            const int row = it / per, m = it - row * per;
-            // the two runs of the item: a half-layout pair block, or neighbours
-            const bool pair = halves && m * VEC < half;
-            const int o1 = pair ? m * VEC : 2 * m * VEC;
-            const int o2 = pair ? m * VEC + half : o1 + VEC;
-            const T* xr = x + row * a.x_ts;
-            if (VEC == 8) {
-                const Pack<T, VEC> p1 = *reinterpret_cast<const Pack<T, VEC>*>(xr + o1);
-                const Pack<T, VEC> p2 = *reinterpret_cast<const Pack<T, VEC>*>(xr + o2);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    val[i][e] = to_f(p1.v[e]);
-                    val[i][VEC + e] = to_f(p2.v[e]);
-                }
-            } else {
-                val[i][0] = to_f(xr[o1]);
-                val[i][1] = to_f(xr[o2]);
-            }
-            if (turn) {
-                const int64_t pos = lo_pos + row;
-                if (pair || VEC == 1) {
-                    if (pair || (!halves && o1 < rot)) {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            float c, s;
-                            rope_angle(rope.turns[pair ? m * VEC + e : m], pos, c, s);
-                            const float x1 = val[i][e], x2 = val[i][VEC + e];
-                            val[i][e] = rope.amplitude * (x1 * c - x2 * s);
-                            val[i][VEC + e] = rope.amplitude * (x2 * c + x1 * s);
-                        }
-                    }
-                } else if (!halves) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {  // pairs of the 2 VEC neighbours
-                        if (o1 + 2 * e < rot) {
-                            float c, s;
-                            rope_angle(rope.turns[m * VEC + e], pos, c, s);
-                            const float x1 = val[i][(2 * e) % (2 * VEC)], x2 = val[i][(2 * e + 1) % (2 * VEC)];
-                            val[i][(2 * e) % (2 * VEC)] = rope.amplitude * (x1 * c - x2 * s);
-                            val[i][(2 * e + 1) % (2 * VEC)] = rope.amplitude * (x2 * c + x1 * s);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2 * VEC; ++e) top = max_nan(top, fabsf(val[i][e]));
-        }
-    }
-    if (!(top <= kLargest)) {  // NaN: 0; up to 2^127, so that scale x code stays finite
-        top = 0.f;
+    const int shift = (v.d == 128 ? 6 : 5) - (VEC == 8 ? 3 : 0);  // log2 of the items of a row
+    const int n = rows << shift, half = rope.rot / 2;
+    using P = Pack<T, VEC>;
+    const T* src[NI];   // the first run of the item in the next head
+    int o1[NI], gap[NI];  // its coordinate, the second run's distance
+    P p1[NI], p2[NI];
+    bool on[NI], pair[NI];
+    float2 cs[VEC == 8 ? NI : 1][VEC];
+    auto fetch = [&]() {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            if ((int)(threadIdx.x + i * blockDim.x) >= n) continue;
-#pragma unroll
-            for (int e = 0; e < 2 * VEC; ++e) {
-                const float y = val[i][e];
-                val[i][e] = y == y ? fminf(fmaxf(y, -kLargest), kLargest) : 0.f;
-                top = fmaxf(top, fabsf(val[i][e]));
-            }
+            if (!on[i]) continue;
+            p1[i] = *reinterpret_cast<const P*>(src[i]);
+            p2[i] = *reinterpret_cast<const P*>(src[i] + gap[i]);
+            src[i] += a.x_hs;
         }
-    }
+    };
+    // amplitude (cos, sin) of the item's pairs: coordinates o1 + e and o1 + gap + e
+    // (half layout), or neighbours, those of the first run and then of the second
+    auto angles = [&](int i, float2 (&w)[VEC]) {
+        const int64_t pos = lo_pos + ((threadIdx.x + i * blockDim.x) >> shift);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, s_red[w]);
-    const float s = fmaxf(s_old, __fdiv_rn(top, code_max<FMT>()));
-    if (threadIdx.x == 0) a.scale[kv][ph] = s;
-    // (below fp32's normal range a reciprocal may overflow: all times 2^64)
-    const float up = s < 1.17549435e-38f ? 18446744073709551616.f : 1.f;
-    const float inv = s > 0.f ? __frcp_rn(s * up) : 0.f;
-    if (up != 1.f) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * VEC; ++e) val[i][e] *= up;
-    }
-
+        for (int e = 0; e < VEC; ++e) {
+            int k = o1[i] + e;
+            if (ROPE == 2)
+                k = VEC == 1 ? o1[i] / 2 : e < VEC / 2 ? o1[i] / 2 + e : (o1[i] + gap[i] - VEC) / 2 + e;
+            float c = 1.f, s = 0.f;
+            if (k < half) rope_angle(rope.turns[k], pos, c, s);
+            w[e] = make_float2(rope.amplitude * c, rope.amplitude * s);
+        }
+    };
+    // pair e of an interleaved item is turned (its coordinates lie within rot)
+    auto turned = [&](int i, int e) {
+        return VEC == 1 ? o1[i] < rope.rot : (e < VEC / 2 ? o1[i] + 2 * e : o1[i] + gap[i] + 2 * e - VEC) < rope.rot;
+    };
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int it = threadIdx.x + i * blockDim.x;
-        if (it < n) {
-            const int row = it / per, m = it - row * per;
-            const bool pair = halves && m * VEC < half;
-            const int o1 = pair ? m * VEC : 2 * m * VEC;
-            const int o2 = pair ? m * VEC + half : o1 + VEC;
-            uint8_t* cr = codes + (row0 + row) * v.d;
+        on[i] = it < n;
+        const int row = it >> shift, m = (it - (row << shift)) * VEC;
+        pair[i] = ROPE == 1 && turn && m < half;
+        const int from = ROPE == 1 && turn ? rope.rot : 0;  // coordinates that are left to the plain items
+        o1[i] = pair[i] || from == 0 ? m : from + m - half;
+        gap[i] = pair[i] ? half : (v.d - from) / 2;
+        if (VEC == 1 && ROPE == 2) {  // a neighbour pair
+            o1[i] = 2 * m;
+            gap[i] = 1;
+        }
+        src[i] = x + row * a.x_ts + o1[i];
+    }
+    fetch();
+    if (VEC == 8 && ROPE && turn) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (on[i] && (ROPE == 2 || pair[i])) angles(i, cs[VEC == 8 ? i : 0]);
+    }
+
+    for (int h = h0; h < h1; ++h) {
+        const int64_t ph = ph0 + h;
+        const float s_old = row0 > 0 ? a.scale[kv][ph] : 0.f;
+        float val[NI][2 * VEC];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if (!on[i]) continue;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                val[i][e] = to_f(p1[i].v[e]);
+                val[i][VEC + e] = to_f(p2[i].v[e]);
+            }
+            if (turn && (ROPE == 2 || pair[i])) {
+                if (VEC == 1) angles(i, cs[0]);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int i1 = ROPE == 1 ? e : 2 * e, i2 = ROPE == 1 ? VEC + e : 2 * e + 1;
+                    const float2 w = cs[VEC == 8 ? i : 0][e];
+                    const float x1 = val[i][i1], x2 = val[i][i2];
+                    if (ROPE == 1 || turned(i, e)) {
+                        val[i][i1] = x1 * w.x - x2 * w.y;
+                        val[i][i2] = x2 * w.x + x1 * w.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2 * VEC; ++e) top = max_nan(top, val[i][e]);
+        }
+        if (h + 1 < h1) fetch();
+        if (!(top <= kLargest)) {  // NaN: 0; up to 2^127, so that scale x code stays finite
+            top = 0.f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                if (!on[i]) continue;
+#pragma unroll
+                for (int e = 0; e < 2 * VEC; ++e) {
+                    const float y = val[i][e];
+                    val[i][e] = y == y ? fminf(fmaxf(y, -kLargest), kLargest) : 0.f;
+                    top = fmaxf(top, fabsf(val[i][e]));
+                }
+            }
+        }
+        // (floats >= 0 are ordered as their bits are)
+        uint32_t* red = s_red[h & 1];
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
+        __syncthreads();
+        const uint32_t lane = threadIdx.x & 31;
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < blockDim.x / 32 ? red[lane] : 0u));
+        const float s = fmaxf(s_old, __fdiv_rn(top, code_max<FMT>()));
+        if (threadIdx.x == 0) a.scale[kv][ph] = s;
+        // (below fp32's normal range a reciprocal may overflow: all times 2^64)
+        const float up = s < 1.17549435e-38f ? 18446744073709551616.f : 1.f;
+        const float inv = s > 0.f ? __frcp_rn(s * up) : 0.f;
+        if (up != 1.f) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int e = 0; e < 2 * VEC; ++e) val[i][e] *= up;
+        }
+        uint8_t* codes = a.codes[kv] + (ph << v.page_log2) * v.d;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if (!on[i]) continue;
+            const int row = (threadIdx.x + i * blockDim.x) >> shift;
+            uint8_t* c1 = codes + (row0 + row) * v.d + o1[i];
+            uint8_t* c2 = c1 + gap[i];
             if (VEC == 8) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     w[e] = encode4<FMT>(val[i][4 * e % (2 * VEC)], val[i][(4 * e + 1) % (2 * VEC)],
                                         val[i][(4 * e + 2) % (2 * VEC)], val[i][(4 * e + 3) % (2 * VEC)], inv);
-                *reinterpret_cast<uint2*>(cr + o1) = make_uint2(w[0], w[1]);
-                *reinterpret_cast<uint2*>(cr + o2) = make_uint2(w[2], w[3]);
+                *reinterpret_cast<uint2*>(c1) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2*>(c2) = make_uint2(w[2], w[3]);
             } else {
                 const uint32_t w = encode4<FMT>(val[i][0], val[i][1], 0.f, 0.f, inv);
-                cr[o1] = (uint8_t)w;
-                cr[o2] = (uint8_t)(w >> 8);
+                *c1 = (uint8_t)w;
+                *c2 = (uint8_t)(w >> 8);
             }
         }
-    }
-    if (row0 > 0 && s > s_old) {  // the page's old rows, for the new scale
-        const float f = s_old * up * inv;
-        uint4* w = reinterpret_cast<uint4*>(codes);
-        const int nw = row0 * v.d / 16;
-        for (int i0 = threadIdx.x; i0 < nw; i0 += 4 * blockDim.x) {
-            uint4 c[4];
+        if (row0 > 0 && s > s_old) {  // the page's old rows, for the new scale
+            const float f = s_old * up * inv;
+            uint4* w = reinterpret_cast<uint4*>(codes);
+            const int nw = row0 * v.d / 16;
+            for (int i0 = threadIdx.x; i0 < nw; i0 += 4 * blockDim.x) {
+                uint4 c[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (i0 + e * (int)blockDim.x < nw) c[e] = w[i0 + e * blockDim.x];
+                for (int e = 0; e < 4; ++e)
+                    if (i0 + e * (int)blockDim.x < nw) c[e] = w[i0 + e * blockDim.x];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (i0 + e * (int)blockDim.x >= nw) continue;
-                uint32_t y[4] = {c[e].x, c[e].y, c[e].z, c[e].w};
+                for (int e = 0; e < 4; ++e) {
+                    if (i0 + e * (int)blockDim.x >= nw) continue;
+                    uint32_t y[4] = {c[e].x, c[e].y, c[e].z, c[e].w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float x[4];
-                    decode4<FMT>(y[k], x);
-                    y[k] = encode4<FMT>(x[0], x[1], x[2], x[3], f);
+                    for (int k = 0; k < 4; ++k) {
+                        float z[4];
+                        decode4<FMT>(y[k], z);
+                        y[k] = encode4<FMT>(z[0], z[1], z[2], z[3], f);
+                    }
+                    w[i0 + e * blockDim.x] = make_uint4(y[0], y[1], y[2], y[3]);
                 }
-                w[i0 + e * blockDim.x] = make_uint4(y[0], y[1], y[2], y[3]);
             }
         }
     }
 }
 
 template <typename T, int FMT, int VEC, int NI>
-int append_go(const AppendArgs& a, const tq_rope_params_t& r, int ns, int threads, cudaStream_t s) {
+int append_go(AppendArgs a, const tq_rope_params_t& r, int ns, int threads, cudaStream_t s) {
     const int64_t gx = (int64_t)ns * a.ppb;
     if (gx > 0x7fffffff) return TQ_ERR_UNSUPPORTED;
-    return launch_behind(k_append<T, FMT, VEC, NI>, dim3((unsigned)gx, (unsigned)a.v.heads, 2), threads, 0,
-                         s, a, r);
+    // heads a block: as many as leave every SM 16 blocks
+    const int64_t share = gx * a.v.heads * 2 / (148 * 16);
+    a.hb = (int)(share < 1 ? 1 : share > 8 ? 8 : share);
+    const int parts = (a.v.heads + a.hb - 1) / a.hb;
+    a.hb = (a.v.heads + parts - 1) / parts;
+    const dim3 grid((unsigned)gx, (unsigned)parts, 2);
+    auto kernel = !a.rope || r.rot == 0 ? k_append<T, FMT, VEC, NI, 0>
+                  : r.layout == TQ_ROPE_HALF ? k_append<T, FMT, VEC, NI, 1> : k_append<T, FMT, VEC, NI, 2>;
+    return launch_behind(kernel, grid, threads, 0, s, a, r);
 }
 
 // Threads and items a thread for the most rows that a block can get.
@@ -247,9 +285,7 @@ int append_fmt(const AppendArgs& a, const tq_rope_params_t& r, int ns, int max_n
     if (wide) {
         const int items = rows * a.v.d / 16;
         if (items <= 128) return append_go<T, FMT, 8, 1>(a, r, ns, 128, s);
-        if (items <= 256) return append_go<T, FMT, 8, 1>(a, r, ns, 256, s);
-        if (items <= 512) return append_go<T, FMT, 8, 2>(a, r, ns, 256, s);
-        return append_go<T, FMT, 8, 4>(a, r, ns, 256, s);
+        return append_go<T, FMT, 8, 1>(a, r, ns, items <= 256 ? 256 : items <= 512 ? 512 : 1024, s);
     }
     const int items = rows * a.v.d / 2;
     if (items <= 256) return append_go<T, FMT, 1, 1>(a, r, ns, 256, s);
