@@ -516,27 +516,30 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         }
                         const uint8_t* src = sm.raw[b];
                         uint8_t* dst = sm.kv[slot];
-#pragma unroll 4
+                        // chunk c of rows r0, r0 + 128 / CH, ..: the swizzles do not change
+                        const int c = tid % CH, r0 = tid / CH, c0 = (c & 3) * 2;
+                        const uint32_t from = r0 * D + ((D == 128 ? c ^ (r0 & 7) : c ^ ((r0 >> 1) & 3)) << 4);
+                        const uint32_t to = (c >> 2) * kBlock + r0 * 128;
+                        // the second block's lanes write in the other order: no bank twice
+                        const uint32_t swap = c >= 4;
+                        const uint32_t p0 = to + (((c0 + swap) ^ (r0 & 7)) << 4);
+                        const uint32_t p1 = to + (((c0 + 1 - swap) ^ (r0 & 7)) << 4);
+                        uint4 x[CH];
+#pragma unroll
                         for (int i = 0; i < CH; ++i) {
-                            const int idx = tid + 128 * i, r = idx / CH, c = idx % CH;
-                            const uint32_t off = D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4))
-                                                          : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-                            uint4 x = *reinterpret_cast<const uint4*>(src + off);
-                            uint4 y0, y1;
+                            x[i] = *reinterpret_cast<const uint4*>(src + from + i * (128 / CH) * D);
                             // rows behind the slot's end: 0 (e4m3 rubbish may be NaN)
-                            if (FMT == TQ_KV_E4M3 && key0 + r >= e.len) x = make_uint4(0, 0, 0, 0);
-                            codes_to_half<FMT>(x.x, y0.x, y0.y);
-                            codes_to_half<FMT>(x.y, y0.z, y0.w);
-                            codes_to_half<FMT>(x.z, y1.x, y1.y);
-                            codes_to_half<FMT>(x.w, y1.z, y1.w);
-                            uint8_t* d = dst + (c >> 2) * kBlock + r * 128;
-                            const int c0 = (c & 3) * 2;
-                            uint4* p0 = reinterpret_cast<uint4*>(d + ((c0 ^ (r & 7)) << 4));
-                            uint4* p1 = reinterpret_cast<uint4*>(d + (((c0 + 1) ^ (r & 7)) << 4));
-                            // the second block's lanes write in the other order: no bank twice
-                            const bool swap = c >= 4;
-                            *(swap ? p1 : p0) = swap ? y1 : y0;
-                            *(swap ? p0 : p1) = swap ? y0 : y1;
+                            if (FMT == TQ_KV_E4M3 && key0 + r0 + i * (128 / CH) >= e.len) x[i] = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < CH; ++i) {
+                            uint4 y0, y1;
+                            codes_to_half<FMT>(x[i].x, y0.x, y0.y);
+                            codes_to_half<FMT>(x[i].y, y0.z, y0.w);
+                            codes_to_half<FMT>(x[i].z, y1.x, y1.y);
+                            codes_to_half<FMT>(x[i].w, y1.z, y1.w);
+                            *reinterpret_cast<uint4*>(dst + p0 + i * (128 / CH) * 128) = swap ? y1 : y0;
+                            *reinterpret_cast<uint4*>(dst + p1 + i * (128 / CH) * 128) = swap ? y0 : y1;
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
