@@ -162,12 +162,6 @@ __device__ __forceinline__ uint32_t swz(int r, int ch) {
                     : (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
 }
 
-// Quotient of non-negative numbers; 64-bit division is a subroutine of some
-// hundred cycles, and the numbers mostly fit 32.
-__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
-    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // Steps of batch entry i: heads x tiles (one tile at least, so that rows without
 // keys are written); none where it has no rows, or too many for this kernel.
 struct Span {
@@ -904,6 +898,8 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
         return TQ_ERR_ARG;
     if (!d_slots && ns > c->slots) return TQ_ERR_ARG;
     if (heads_q % c->heads || heads_q / c->heads > 128) return TQ_ERR_UNSUPPORTED;
+    // rows (tokens x group) count in 32 bits
+    if (total_q >= ((int64_t)1 << 31) / (heads_q / c->heads) - 512) return TQ_ERR_UNSUPPORTED;
     if (ns == 0 || total_q == 0 || max_q == 0) return TQ_OK;
     if (!d_cu || !d_q || !d_out || (((uintptr_t)d_q | (uintptr_t)d_out) & 15u) || q_ts % 8 || q_hs % 8)
         return TQ_ERR_ARG;

@@ -73,6 +73,12 @@ __device__ __forceinline__ int below_window(const Attn& a, int pos) {
     return a.window > 0 ? (int)max((int64_t)-1, (int64_t)pos - a.window) : -1;
 }
 
+// Quotient of non-negative numbers; 64-bit division is a subroutine of some
+// hundred cycles, and the numbers mostly fit 32.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -22,9 +22,13 @@
 //             MN-major), with the tile's scales.
 //   12        issues the MMAs: per tile and stage O += P V of this tile, then S of
 //             the next, so each stage's softmax hides behind the other's MMAs.
-//   13        the TMA loads, a page table lookup a box.
+//   13        the TMA loads, a page table lookup a box, a tile ahead.
+//   14        walks the CTA's share and hands the others its items, with R, through
+//             a short ring: lengths, divisions and lookups are off their path.
 // Every wait is bounded (1 s); a warp that gives up sets the abort flag and the
 // call's status.
+#include <type_traits>
+
 #include "tq_kv8_attention.cuh"
 #include "tq_score_common.cuh"
 
@@ -42,8 +46,20 @@ constexpr int kPRows = 2 * kPM;     // rows an item
 constexpr int kPThreads = 512;
 constexpr int kGroups = kPT / 16;   // scale groups of a tile
 constexpr int kRing = 4;            // tiles whose scales are kept
+constexpr int kWorks = 4;           // items that are handed out ahead
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGrow = 8.f;        // log2 of how far P may pass 1
+
+// A CTA's piece of an item, as the warps get it.
+struct Work {
+    int slot, len, head;
+    int pos0;         // position of the entry's first query: len - its queries
+    int row0, rows;   // first of the item's rows (token x group), their number; 0: no more work
+    int t0, t, t_end, nt;  // first tile of the item; the CTA's tiles t .. t_end of its nt
+    int parts;        // CTAs that hold the item, where it begins here and goes on
+    float R;          // largest value scale of the CTA's keys
+    int64_t c0;       // the entry's first query token
+};
 
 template <int D>
 struct PSmem {
@@ -52,91 +68,78 @@ struct PSmem {
     uint8_t raw[2][kPT * D];      // codes as they arrive: K, V
     float kscale[kRing][kGroups], vscale[kRing][kGroups];  // s_k, s_v / R
     uint32_t absent[kRing];       // 16-key groups without a page
-    float rmax[kRing];            // R of the tile's item
-    float red[4];
+    Work work[kWorks];
     uint64_t raw_full[2], raw_empty[2], kv_full[4], kv_empty[4];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], mma_done;
+    uint64_t work_full[kWorks], work_empty[kWorks];
     uint32_t tmem_base;
     int abort;
 };
 
-// Item of the batch: 256 rows `part` of head `head` of entry `i`.
-struct Item {
-    Entry e;
-    int i, head, part, t0, nt;
-    int64_t per_head;  // tiles of all parts of a head
-};
-
+// (rows of a call, tokens x group, count in 32 bits)
 __device__ __forceinline__ int parts_of(const Attn& a, const Entry& e) {
-    const int64_t rows = (int64_t)e.qn * a.group;
-    return rows > a.few ? (int)((rows + kPRows - 1) / kPRows) : 0;
+    const int rows = e.qn * a.group;
+    return rows > a.few ? (rows + kPRows - 1) / kPRows : 0;
 }
 // First tile and number of tiles of a part (one at least: rows without keys are
 // written too).
 __device__ __forceinline__ void tiles_of(const Attn& a, const Entry& e, int part, int& t0, int& nt) {
-    const int first = (int)((int64_t)part * kPRows / a.group);
-    const int last = (int)min((int64_t)e.qn - 1, ((int64_t)(part + 1) * kPRows - 1) / a.group);
+    const int first = (unsigned)(part * kPRows) / (unsigned)a.group;
+    const int last = min(e.qn - 1, (int)(((unsigned)(part + 1) * kPRows - 1) / (unsigned)a.group));
     const int end = a.causal ? min(e.len, e.len - e.qn + last + 1) : e.len;
     const int beg = below_window(a, e.len - e.qn + first) + 1;
     t0 = beg / kPT;
     nt = max(1, (end + kPT - 1) / kPT - t0);
 }
-__device__ __forceinline__ int64_t tiles_per_head(const Attn& a, const Entry& e) {
+// Tiles of all parts of a head: part i, i + step, ..
+__device__ __forceinline__ int64_t tiles_per_head(const Attn& a, const Entry& e, int i, int step) {
     int64_t n = 0;
-    for (int p = 0, m = parts_of(a, e); p < m; ++p) {
+    for (const int m = parts_of(a, e); i < m; i += step) {
         int t0, nt;
-        tiles_of(a, e, p, t0, nt);
+        tiles_of(a, e, i, t0, nt);
         n += nt;
     }
     return n;
 }
-// To step `rem` of entry i's steps; returns the tile within the item.
-__device__ __forceinline__ int open_item(const Attn& a, Item& it, int64_t rem) {
-    it.head = (int)(rem / it.per_head);
-    rem -= it.head * it.per_head;
-    it.part = 0;
-    while (true) {
-        tiles_of(a, it.e, it.part, it.t0, it.nt);
-        if (rem < it.nt) return (int)rem;
-        rem -= it.nt;
-        ++it.part;
-    }
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
 }
-__device__ __forceinline__ void next_item(const Attn& a, Item& it) {
-    if (++it.part < parts_of(a, it.e)) {
-        tiles_of(a, it.e, it.part, it.t0, it.nt);
-        return;
-    }
-    it.part = 0;
-    if (++it.head == a.v.heads) {
-        it.head = 0;
-        do {
-            it.e = entry_of(a, ++it.i);
-        } while (parts_of(a, it.e) == 0);
-        it.per_head = tiles_per_head(a, it.e);
-    }
-    tiles_of(a, it.e, it.part, it.t0, it.nt);
-}
-
-// A CTA's share of the steps, walked item by item.  Every role walks it alone.
-struct Walk {
-    Item it;
-    int t, t_end;      // tiles of the item that are this CTA's
-    int64_t g, g1;
-    __device__ __forceinline__ bool done() const { return g >= g1; }
-    __device__ __forceinline__ void clip() { t_end = (int)min((int64_t)it.nt, t + (g1 - g)); }
-    __device__ __forceinline__ void next(const Attn& a) {
-        g += t_end - t;
-        if (g >= g1) return;
-        next_item(a, it);
-        t = 0;
-        clip();
-    }
-};
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max16(const uint32_t* s) {
+    auto f = [&](int i) { return __uint_as_float(s[i]); };
+    const float a = max3(max3(f(0), f(1), f(2)), f(3), f(4)), b = max3(max3(f(5), f(6), f(7)), f(8), f(9));
+    return max3(max3(a, f(10), f(11)), max3(b, f(12), f(13)), fmaxf(f(14), f(15)));
+}
+
+// 2^x for x <= 126 on the FMA pipe (below -126: 2^-126): x = n + f with |f| <= 1/2,
+// 2^f by the degree-5 Chebyshev expansion (within 2^-23), n into the exponent.  The
+// exponential unit alone (16 a clock) would take as long as the MMAs of a tile.
+constexpr int kPoly = 2;  // of 8 pairs
+__device__ __forceinline__ float2 exp2_pair(float2 x) {
+    auto both = [](float v) { return make_float2(v, v); };
+    x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
+    const float2 t = __fadd2_rn(x, both(12582912.f));  // n in the last bits
+    const float2 n = __fadd2_rn(t, both(-12582912.f));
+    const float2 f = ffma2(n, both(-1.f), x);
+    float2 p = ffma2(f, both(0.0013427354f), both(0.009673781f));
+    p = ffma2(p, f, both(0.05550341f));
+    p = ffma2(p, f, both(0.24022229f));
+    p = ffma2(p, f, both(0.6931472f));
+    p = ffma2(p, f, both(1.f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
 template <int N>
@@ -162,13 +165,23 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
     const int unit = blockIdx.x;
     grid_begin();
 
-    // ---- the batch's steps: a run of entries a thread, prefix over the block
+    // ---- the batch's steps: a run of entries a thread (few entries: a warp an
+    // entry), prefix over the block
     int64_t* pre = reinterpret_cast<int64_t*>(sm.kv);  // (before the operands are)
     const int run = (a.ns + kPThreads - 1) / kPThreads;
     {
         int64_t mine = 0;
-        for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i)
-            mine += a.v.heads * tiles_per_head(a, entry_of(a, i));
+        if (a.ns <= 32) {
+            for (int i = warp; i < a.ns; i += kPThreads / 32) {
+                const int64_t n = warp_sum(tiles_per_head(a, entry_of(a, i), lane, 32));
+                if (lane == 0) pre[kPThreads + 1 + i] = a.v.heads * n;
+            }
+            __syncthreads();
+            if ((int)threadIdx.x < a.ns) mine = pre[kPThreads + 1 + threadIdx.x];
+        } else {
+            for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i)
+                mine += a.v.heads * tiles_per_head(a, entry_of(a, i), 0, 1);
+        }
         if (threadIdx.x == 0) {
             sm.abort = 0;
             for (int i = 0; i < 2; ++i) {
@@ -183,8 +196,15 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 mbar_init(&sm.kv_full[i], 4);
                 mbar_init(&sm.kv_empty[i], 1);
             }
+            for (int i = 0; i < kWorks; ++i) {
+                mbar_init(&sm.work_full[i], 1);
+                mbar_init(&sm.work_empty[i], 14);  // all warps but the scheduler's own and the idle one
+            }
             mbar_init(&sm.mma_done, 1);
             fence_mbar_init();
+            prefetch_tmap(&kmap);
+            prefetch_tmap(&vmap);
+            parts.cut[unit].parts = 0;
         }
         int64_t inc = mine;
 #pragma unroll
@@ -192,42 +212,31 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
         }
+        int64_t* sums = pre + kPThreads + 40;
+        if (lane == 31) sums[warp] = inc;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) inc += sums[w];
         pre[threadIdx.x + 1] = inc;
-        __syncthreads();
-        int64_t before = 0;
-        for (int w = 0; w < warp; ++w) before += pre[32 * w + 32];
-        __syncthreads();
-        pre[threadIdx.x + 1] = inc + before;
-        if (threadIdx.x == 0) {
-            pre[0] = 0;
-            parts.cut[unit].parts = 0;
-        }
+        if (threadIdx.x == 0) pre[0] = 0;
         __syncthreads();
     }
+    // the first `rest` CTAs take base + 1 steps, the others base
     const int64_t total = pre[kPThreads];
-    const int64_t units = min((int64_t)gridDim.x, total);
-    Walk w = {};
-    if (unit < units) {
-        w.g = unit * total / units;
-        w.g1 = (unit + 1) * total / units;
-        int lo = 0, hi = kPThreads;  // the run of entries that holds step g
+    const int units = (int)min((int64_t)gridDim.x, total);
+    const int64_t base = units ? quot(total, units) : 0, rest = total - base * units;
+    const int64_t g0 = unit < units ? unit * base + min((int64_t)unit, rest) : 0;
+    const int64_t g1 = unit < units ? g0 + base + (unit < rest ? 1 : 0) : 0;
+    int entry = 0;
+    int64_t rem = 0;  // step g0 is step `rem` of entry `entry` and those behind it
+    if (warp == 14 && g0 < g1) {
+        int lo = 0, hi = (a.ns + run - 1) / run;  // the run of entries that holds step g0
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= w.g) lo = mid;
+            if (pre[mid] <= g0) lo = mid;
             else hi = mid;
         }
-        int64_t rem = w.g - pre[lo];
-        int i = lo * run;
-        while (true) {
-            w.it.e = entry_of(a, i);
-            w.it.per_head = tiles_per_head(a, w.it.e);
-            if (rem < w.it.per_head * a.v.heads) break;
-            rem -= w.it.per_head * a.v.heads;
-            ++i;
-        }
-        w.it.i = i;
-        w.t = open_item(a, w.it, rem);
-        w.clip();
+        rem = g0 - pre[lo];
+        entry = lo * run;
     }
     if (warp == 12) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -247,6 +256,13 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
         return true;
     };
 
+    // the n-th piece of work
+    auto get = [&](uint32_t n) { return wait(&sm.work_full[n % kWorks], n / kWorks & 1); };
+    auto done_with = [&](uint32_t n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.work_empty[n % kWorks]);
+    };
+
     if (warp < 8) {
         // ================================================== softmax, a row a thread
         regs_up<192>();
@@ -255,22 +271,23 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
         const uint32_t s_col = lane_addr + st * kPT, o_col = lane_addr + 2 * kPT + st * D;
         uint32_t tile = 0, n_s = 0, n_o = 0;  // tiles so far; waits on s_full, o_full
         bool ok = true;
-        for (; !w.done() && ok; w.next(a)) {
-            const Item& it = w.it;
-            const Entry& e = it.e;
-            const int64_t rows = (int64_t)e.qn * a.group;
-            const int64_t ri = (int64_t)it.part * kPRows + st * kPM + row;
-            if ((int64_t)it.part * kPRows + st * kPM >= rows) {  // the item has one stage
-                tile += w.t_end - w.t;
+        for (uint32_t n = 0; ok && (ok = get(n)); ++n) {
+            const Work& w = sm.work[n % kWorks];
+            if (w.rows == 0) break;
+            const int t_begin = w.t, t_end = w.t_end;
+            if (st * kPM >= w.rows) {  // the item has one stage
+                tile += t_end - t_begin;
+                done_with(n);
                 continue;
             }
-            const bool valid = ri < rows;
-            const int tq = valid ? (int)(ri / a.group) : 0;
-            const int hq = it.head * a.group + (valid ? (int)(ri - (int64_t)tq * a.group) : 0);
+            const bool valid = st * kPM + row < w.rows;
+            const unsigned ri = w.row0 + (valid ? st * kPM + row : 0);
+            const int tq = ri / (unsigned)a.group, hq = w.head * a.group + (int)(ri - tq * a.group);
+            const int64_t tok = w.c0 + tq;
             // ---- the query row, as halves
             float sl;
             {
-                const T* q = (const T*)a.q + (e.c0 + tq) * a.q_ts + (int64_t)hq * a.q_hs;
+                const T* q = (const T*)a.q + tok * a.q_ts + (int64_t)hq * a.q_hs;
                 Pack<T, 8> x[D / 8];
                 float top = 0.f;
 #pragma unroll
@@ -302,13 +319,12 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.q_full[st]);
             }
-            const int pos = e.len - e.qn + tq;
-            const int lim = !valid ? e.len - 1 : a.causal ? min(pos, e.len - 1) : e.len - 1;
+            const int pos = w.pos0 + tq, len = w.len;
+            const int lim = valid && a.causal ? min(pos, len - 1) : len - 1;
             const int low = valid ? below_window(a, pos) : -1;
-            float m = -INFINITY, R = 0.f;
+            float m = -INFINITY;
             float2 L2 = make_float2(0.f, 0.f);
-            for (int t = w.t; t < w.t_end; ++t, ++tile) {
-                const int key0 = (it.t0 + t) * kPT;
+            for (int t = t_begin, key0 = (w.t0 + t_begin) * kPT; t < t_end; ++t, ++tile, key0 += kPT) {
                 const int rg = tile & (kRing - 1);
                 if (!wait(&sm.s_full[st], n_s & 1)) {
                     ok = false;
@@ -317,32 +333,38 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 ++n_s;
                 tc_fence_after();
                 uint32_t s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, s[c]);
+                tmem_ld32(s_col, s[0]);
                 float cg[kGroups];
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) cg[g] = sl * sm.kscale[rg][g];
                 const uint32_t absent = sm.absent[rg];
-                if (t == w.t) R = sm.rmax[rg];
-                tmem_wait_ld();
-                if (__any_sync(0xffffffffu, key0 + kPT - 1 > lim || key0 <= low || absent)) {
+                const bool masked = __any_sync(0xffffffffu, key0 + kPT - 1 > lim || key0 <= low || absent);
+                float top = -INFINITY;
+                // 32 keys are on their way while the 32 before them are looked at
+                if (masked) {
 #pragma unroll
-                    for (int i = 0; i < kPT; ++i) {
-                        const int key = key0 + i;
-                        const bool see = key <= lim && key > low && !(absent >> (i / 16) & 1u);
-                        s[i / 32][i % 32] = see ? __float_as_uint(__uint_as_float(s[i / 32][i % 32]) * cg[i / 16])
-                                                : 0xff800000u;
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        if (c < 3) tmem_ld32(s_col + 32 * (c + 1), s[c + 1]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int key = key0 + 32 * c + i;
+                            const bool see = key <= lim && key > low && !(absent >> (2 * c + i / 16) & 1u);
+                            const float x = see ? __uint_as_float(s[c][i]) * cg[2 * c + i / 16] : -INFINITY;
+                            s[c][i] = __float_as_uint(x);
+                            top = fmaxf(top, x);
+                        }
                     }
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) cg[g] = 1.f;
-                }
-                float top = -INFINITY;
+                } else {
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    float x = __uint_as_float(s[g / 2][(g & 1) * 16]);
-#pragma unroll
-                    for (int i = 1; i < 16; ++i) x = fmaxf(x, __uint_as_float(s[g / 2][(g & 1) * 16 + i]));
-                    top = fmaxf(top, x * cg[g]);
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        if (c < 3) tmem_ld32(s_col + 32 * (c + 1), s[c + 1]);
+                        const float x0 = max16(&s[c][0]) * cg[2 * c], x1 = max16(&s[c][16]) * cg[2 * c + 1];
+                        top = max3(top, x0, x1);
+                    }
                 }
                 // the reference follows when the maximum has grown past it by kGrow
                 const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
@@ -353,7 +375,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     L2.x *= shrink;
                     L2.y *= shrink;
                 }
-                if (t > w.t && __any_sync(0xffffffffu, grow)) {
+                if (t > t_begin && __any_sync(0xffffffffu, grow)) {
                     // S of this tile is complete, so O += P V of the last one is too
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -366,29 +388,37 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     }
                 }
                 const float base = m == -INFINITY ? 0.f : -m;
+                auto probabilities = [&](auto some) {  // some: pairs of 8 that go to the polynomial
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t p[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int g = 2 * c + h;
-                        const float vw = sm.vscale[rg][g];
-                        const float2 cc = make_float2(cg[g], cg[g]), bb = make_float2(base, base);
-                        const float2 ww = make_float2(vw, vw);
+                        for (int h = 0; h < 2; ++h) {
+                            const int g = 2 * c + h;
+                            const float vw = sm.vscale[rg][g];
+                            const float2 cc = make_float2(cg[g], cg[g]), bb = make_float2(base, base);
+                            const float2 ww = make_float2(vw, vw);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float2 x = make_float2(__uint_as_float(s[c][16 * h + 2 * i]),
-                                                   __uint_as_float(s[c][16 * h + 2 * i + 1]));
-                            x = ffma2(x, cc, bb);
-                            x.x = ex2(x.x);
-                            x.y = ex2(x.y);
-                            L2 = __fadd2_rn(L2, x);
-                            x = __fmul2_rn(x, ww);
-                            p[8 * h + i] = half2_bits(x.x, x.y);
+                            for (int i = 0; i < 8; ++i) {
+                                float2 x = make_float2(__uint_as_float(s[c][16 * h + 2 * i]),
+                                                       __uint_as_float(s[c][16 * h + 2 * i + 1]));
+                                x = ffma2(x, cc, bb);
+                                if (i % 4 < some / 2) {
+                                    x = exp2_pair(x);
+                                } else {
+                                    x.x = ex2(x.x);
+                                    x.y = ex2(x.y);
+                                }
+                                L2 = __fadd2_rn(L2, x);
+                                x = __fmul2_rn(x, ww);
+                                p[8 * h + i] = half2_bits(x.x, x.y);
+                            }
                         }
+                        tmem_st16(s_col + 16 * c, p);
                     }
-                    tmem_st16(s_col + 16 * c, p);
-                }
+                };
+                if (masked) probabilities(std::integral_constant<int, 0>{});
+                else probabilities(std::integral_constant<int, kPoly>{});
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -402,56 +432,57 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             ++n_o;
             tc_fence_after();
             const float L = L2.x + L2.y;
-            const bool begins = w.t == 0, ends = w.t_end == it.nt;
+            const bool begins = t_begin == 0, ends = t_end == w.nt;
+            const float R = w.R;
             if (begins && ends) {
-                const float n = L > 0.f ? R / L : (L == 0.f ? 0.f : L);
-                T* out = (T*)a.out + ((e.c0 + tq) * a.heads_q + hq) * D;
+                const float f = L > 0.f ? R / L : (L == 0.f ? 0.f : L);
+                T* out = (T*)a.out + (tok * a.heads_q + hq) * D;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(o_col + c, o);
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_col + c, o);
                     tmem_wait_ld();
                     if (valid) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < 4; ++h) {
                             Pack<T, 8> y;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) from_f(__uint_as_float(o[8 * h + k]) * n, y.v[k]);
+                            for (int k = 0; k < 8; ++k) from_f(__uint_as_float(o[8 * h + k]) * f, y.v[k]);
                             *reinterpret_cast<Pack<T, 8>*>(out + c + 8 * h) = y;
                         }
                     }
                 }
                 if (a.lse && valid)
-                    a.lse[(e.c0 + tq) * a.heads_q + hq] = L > 0.f ? (m + log2f(L)) * 0.69314718056f : (L == 0.f ? -INFINITY : L);
+                    a.lse[tok * a.heads_q + hq] = L > 0.f ? (m + log2f(L)) * 0.69314718056f : (L == 0.f ? -INFINITY : L);
             } else {
                 const int64_t slot = 2 * (int64_t)unit + (begins ? 1 : 0);
                 const int64_t pr = slot * kPRows + st * kPM + row;
                 if (valid) parts.ml[pr] = make_float2(m, L);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(o_col + c, o);
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_col + c, o);
                     tmem_wait_ld();
                     if (valid) {
 #pragma unroll
-                        for (int k = 0; k < 16; k += 4)
+                        for (int k = 0; k < 32; k += 4)
                             *reinterpret_cast<float4*>(parts.o + pr * D + c + k) =
                                 make_float4(__uint_as_float(o[k]) * R, __uint_as_float(o[k + 1]) * R,
                                             __uint_as_float(o[k + 2]) * R, __uint_as_float(o[k + 3]) * R);
                     }
                 }
                 if (begins && st == 0 && row == 0) {
-                    const int64_t last = w.g + it.nt - 1;  // the item's last step: its CTA
                     Cut c;
-                    c.parts = (int)(((last + 1) * units - 1) / total) - unit + 1;
-                    c.rows = (int)min((int64_t)kPRows, rows - (int64_t)it.part * kPRows);
-                    c.head = it.head;
+                    c.parts = w.parts;
+                    c.rows = w.rows;
+                    c.head = w.head;
                     c.pad = 0;
-                    c.row0 = e.c0 * a.group + (int64_t)it.part * kPRows;
+                    c.row0 = w.c0 * a.group + w.row0;
                     parts.cut[unit] = c;
                 }
             }
             tc_fence_before();  // O is read before the next item's MMAs write it
+            done_with(n);
         }
     } else {
         regs_down<64>();
@@ -460,46 +491,34 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             const int tid = threadIdx.x - 256;
             uint32_t tile = 0, n_raw = 0;
             bool ok = true;
-            for (; !w.done() && ok; w.next(a)) {
-                const Item& it = w.it;
-                const Entry& e = it.e;
-                // R: the largest value scale of the keys of this CTA's part
-                const int k0 = (it.t0 + w.t) * kPT, k1 = min(e.len, (it.t0 + w.t_end) * kPT);
-                float R = 0.f;
-                for (int p = (k0 >> a.v.page_log2) + tid; p <= (k1 - 1) >> a.v.page_log2 && k1 > k0; p += 128) {
-                    const int pid = page_of(a.v, e.slot, p);
-                    if (pid >= 0) R = fmaxf(R, a.vs[(int64_t)pid * a.v.heads + it.head]);
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
-                if (lane == 0) sm.red[warp - 8] = R;
-                named_bar(1, 128);
-                R = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
-                named_bar(1, 128);
+            for (uint32_t n = 0; ok && (ok = get(n)); ++n) {
+                const Work& w = sm.work[n % kWorks];
+                if (w.rows == 0) break;
+                const int t_end = w.t_end, len = w.len, slot = w.slot, head = w.head, tile0 = w.t0;
                 // (scales below fp32's normal range have no reciprocal: their values count as 0)
-                const float inv = R >= 1.17549435e-38f ? 1.f / R : 0.f;
+                const float inv = w.R >= 1.17549435e-38f ? 1.f / w.R : 0.f;
                 // thread g < 8: s_k of the next tile's 16-key group g; 8..15: s_v; NaN: no page
                 auto load_scale = [&](int t) {
                     float x = 0.f;
                     if (tid < 16) {
-                        const int key = (it.t0 + t) * kPT + 16 * (tid & 7);
-                        const int pid = key < e.len ? page_of(a.v, e.slot, key >> a.v.page_log2) : -1;
-                        if (pid >= 0) x = (tid < 8 ? a.ks : a.vs)[(int64_t)pid * a.v.heads + it.head];
+                        const int key = (tile0 + t) * kPT + 16 * (tid & 7);
+                        const int pid = key < len ? page_of(a.v, slot, key >> a.v.page_log2) : -1;
+                        if (pid >= 0) x = (tid < 8 ? a.ks : a.vs)[(int64_t)pid * a.v.heads + head];
                         else x = tid < 8 ? -1.f : 0.f;
                     }
                     return x;
                 };
                 float next = load_scale(w.t);
-                for (int t = w.t; t < w.t_end && ok; ++t, ++tile) {
-                    const int key0 = (it.t0 + t) * kPT;
+                for (int t = w.t; t < t_end && ok; ++t, ++tile) {
+                    const int key0 = (tile0 + t) * kPT;
                     const float sc = next;
-                    if (t + 1 < w.t_end) next = load_scale(t + 1);
+                    if (t + 1 < t_end) next = load_scale(t + 1);
 #pragma unroll 1
                     for (int isv = 0; isv < 2; ++isv) {
-                        const int slot = 2 * isv + (tile & 1);
+                        const int buf = 2 * isv + (tile & 1);
                         const uint32_t b = n_raw & 1, ph = (n_raw >> 1) & 1;
                         if (!wait(&sm.raw_full[b], ph) ||
-                            (tile >= 2 && !wait(&sm.kv_empty[slot], ((tile >> 1) - 1) & 1))) {
+                            (tile >= 2 && !wait(&sm.kv_empty[buf], ((tile >> 1) - 1) & 1))) {
                             ok = false;
                             break;
                         }
@@ -509,13 +528,10 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                             const uint32_t gone = __ballot_sync(0xffffffffu, tid < 8 && sc < 0.f);
                             if (tid < 8) sm.kscale[rg][tid] = fmaxf(sc, 0.f);
                             else if (tid < 16) sm.vscale[rg][tid - 8] = sc * inv;
-                            if (tid == 0) {
-                                sm.absent[rg] = gone;
-                                sm.rmax[rg] = R;
-                            }
+                            if (tid == 0) sm.absent[rg] = gone;
                         }
                         const uint8_t* src = sm.raw[b];
-                        uint8_t* dst = sm.kv[slot];
+                        uint8_t* dst = sm.kv[buf];
                         // chunk c of rows r0, r0 + 128 / CH, ..: the swizzles do not change
                         const int c = tid % CH, r0 = tid / CH, c0 = (c & 3) * 2;
                         const uint32_t from = r0 * D + ((D == 128 ? c ^ (r0 & 7) : c ^ ((r0 >> 1) & 3)) << 4);
@@ -529,7 +545,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         for (int i = 0; i < CH; ++i) {
                             x[i] = *reinterpret_cast<const uint4*>(src + from + i * (128 / CH) * D);
                             // rows behind the slot's end: 0 (e4m3 rubbish may be NaN)
-                            if (FMT == TQ_KV_E4M3 && key0 + r0 + i * (128 / CH) >= e.len) x[i] = make_uint4(0, 0, 0, 0);
+                            if (FMT == TQ_KV_E4M3 && key0 + r0 + i * (128 / CH) >= len) x[i] = make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
                         for (int i = 0; i < CH; ++i) {
@@ -544,11 +560,12 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(&sm.kv_full[slot]);
+                            mbar_arrive(&sm.kv_full[buf]);
                             mbar_arrive(&sm.raw_empty[b]);
                         }
                     }
                 }
+                done_with(n);
             }
         } else if (warp == 12) {
             // ============================================== MMAs
@@ -578,9 +595,11 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                                    kPV, !(first && k == 0));
                 }
             };
-            for (; !w.done() && ok; w.next(a)) {
-                const int64_t rows = (int64_t)w.it.e.qn * a.group - (int64_t)w.it.part * kPRows;
-                const int nst = rows > kPM ? 2 : 1;
+            for (uint32_t n = 0; ok && (ok = get(n)); ++n) {
+                const Work& w = sm.work[n % kWorks];
+                const int nst = w.rows > kPM ? 2 : 1, tiles = w.t_end - w.t;
+                if (w.rows == 0) break;
+                done_with(n);
                 for (int st = 0; st < nst && ok; ++st) {
                     ok = wait(&sm.q_full[st], n_q[st] & 1);
                     ++n_q[st];
@@ -590,16 +609,17 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 tc_fence_after();
                 for (int st = 0; st < nst; ++st) qk(st, tile);
                 if (lane == 0) tc_commit(&sm.kv_empty[tile & 1]);
-                for (int t = w.t; t < w.t_end && ok; ++t, ++tile) {
-                    const bool more = t + 1 < w.t_end;
-                    if (more) ok = wait(&sm.kv_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
-                    if (ok) ok = wait(&sm.kv_full[2 + (tile & 1)], (tile >> 1) & 1);
+                for (int t = 0; t < tiles && ok; ++t, ++tile) {
+                    const bool more = t + 1 < tiles;
+                    ok = wait(&sm.kv_full[2 + (tile & 1)], (tile >> 1) & 1);
                     for (int st = 0; st < nst && ok; ++st) {
                         ok = wait(&sm.p_full[st], n_p[st] & 1);
                         ++n_p[st];
                         if (!ok) break;
                         tc_fence_after();
-                        pv(st, tile, t == w.t);
+                        pv(st, tile, t == 0);
+                        if (more && st == 0) ok = wait(&sm.kv_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
+                        if (!ok) break;
                         if (more) qk(st, tile + 1);
                         else if (lane == 0) tc_commit(&sm.o_full[st]);
                     }
@@ -619,20 +639,25 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
         } else if (warp == 13) {
             // ============================================== TMA
             const int box = a.v.page, nbox = kPT / box;
-            uint32_t n = 0;
+            uint32_t c = 0;  // copies of a tile's K or V
             bool ok = true;
-            for (; !w.done() && ok; w.next(a)) {
-                const Item& it = w.it;
-                for (int t = w.t; t < w.t_end && ok; ++t) {
-                    const int key = (it.t0 + t) * kPT + lane * box;
-                    int row = a.rows;  // behind the tensor: zeros
-                    if (lane < nbox && key < it.e.len) {
-                        const int pid = page_of(a.v, it.e.slot, key >> a.v.page_log2);
-                        if (pid >= 0) row = (int)(((int64_t)pid * a.v.heads + it.head) << a.v.page_log2);
-                    }
-                    for (int isv = 0; isv < 2; ++isv, ++n) {
-                        const uint32_t b = n & 1;
-                        if (n >= 2 && !wait(&sm.raw_empty[b], ((n >> 1) - 1) & 1)) {
+            for (uint32_t n = 0; ok && (ok = get(n)); ++n) {
+                const Work& w = sm.work[n % kWorks];
+                if (w.rows == 0) break;
+                const int t_end = w.t_end, len = w.len, slot = w.slot, head = w.head, tile0 = w.t0;
+                auto lookup = [&](int t) {
+                    const int key = (tile0 + t) * kPT + lane * box;
+                    return lane < nbox && key < len ? page_of(a.v, slot, key >> a.v.page_log2) : -1;
+                };
+                int t = w.t, next = lookup(t);
+                done_with(n);
+                for (; t < t_end && ok; ++t) {
+                    // (a page that is not there: rows behind the tensor, zeros)
+                    const int row = next >= 0 ? (int)(((int64_t)next * a.v.heads + head) << a.v.page_log2) : a.rows;
+                    if (t + 1 < t_end) next = lookup(t + 1);
+                    for (int isv = 0; isv < 2; ++isv, ++c) {
+                        const uint32_t b = c & 1;
+                        if (c >= 2 && !wait(&sm.raw_empty[b], ((c >> 1) - 1) & 1)) {
                             ok = false;
                             break;
                         }
@@ -645,8 +670,90 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             }
             if (!ok) {  // no copy may land after the block has gone
                 int none = 0;
-                for (uint32_t i = n >= 2 ? n - 2 : 0; i < n; ++i)
+                for (uint32_t i = c >= 2 ? c - 2 : 0; i < c; ++i)
                     mbar_wait(&sm.raw_full[i & 1], (i >> 1) & 1, &none, kWaitNs);
+            }
+        } else if (warp == 14) {
+            // ============================================== the CTA's share, item by item
+            Entry e = {};
+            int head = 0, part = 0, m = 0, t = 0;
+            bool ok = true;
+            if (g0 < g1) {
+                int64_t per_head;
+                while (true) {
+                    e = entry_of(a, entry);
+                    per_head = warp_sum(tiles_per_head(a, e, lane, 32));
+                    if (rem < per_head * a.v.heads) break;
+                    rem -= per_head * a.v.heads;
+                    ++entry;
+                }
+                m = parts_of(a, e);
+                head = (int)quot(rem, per_head);
+                rem -= head * per_head;
+                for (;; part += 32) {  // 32 parts at a time
+                    int t0, nt = 0;
+                    if (part + lane < m) tiles_of(a, e, part + lane, t0, nt);
+                    int64_t inc = nt;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                        if (lane >= o) inc += y;
+                    }
+                    const uint32_t past = __ballot_sync(0xffffffffu, inc > rem);
+                    if (past) {
+                        const int k = __ffs(past) - 1;
+                        t = (int)(rem - (__shfl_sync(0xffffffffu, inc, k) - __shfl_sync(0xffffffffu, nt, k)));
+                        part += k;
+                        break;
+                    }
+                    rem -= __shfl_sync(0xffffffffu, inc, 31);
+                }
+            }
+            uint32_t n = 0;
+            for (int64_t g = g0; ok; ++n) {
+                Work w = {};
+                if (g < g1) {
+                    w.slot = e.slot;
+                    w.len = e.len;
+                    w.head = head;
+                    w.pos0 = e.len - e.qn;
+                    w.row0 = part * kPRows;
+                    w.rows = min(kPRows, e.qn * a.group - w.row0);
+                    w.c0 = e.c0;
+                    tiles_of(a, e, part, w.t0, w.nt);
+                    w.t = t;
+                    w.t_end = (int)min((int64_t)w.nt, t + (g1 - g));
+                    if (t == 0 && w.t_end < w.nt) {
+                        const int64_t last = g + w.nt - 1, head1 = rest * (base + 1);  // the item's last step: its CTA
+                        w.parts = (int)(last < head1 ? quot(last, base + 1) : rest + quot(last - head1, base)) - unit + 1;
+                    }
+                    const int p1 = (min(e.len, (w.t0 + w.t_end) * kPT) - 1) >> a.v.page_log2;
+#pragma unroll 4
+                    for (int p = (((w.t0 + t) * kPT) >> a.v.page_log2) + lane; p <= p1; p += 32) {
+                        const int pid = page_of(a.v, e.slot, p);
+                        if (pid >= 0) w.R = fmaxf(w.R, a.vs[(int64_t)pid * a.v.heads + head]);
+                    }
+                    w.R = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(w.R)));
+                }
+                ok = n < kWorks || wait(&sm.work_empty[n % kWorks], (n / kWorks - 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    sm.work[n % kWorks] = w;
+                    mbar_arrive(&sm.work_full[n % kWorks]);
+                }
+                if (w.rows == 0) break;
+                g += w.t_end - t;
+                t = 0;
+                if (g < g1 && ++part == m) {
+                    part = 0;
+                    if (++head == a.v.heads) {
+                        head = 0;
+                        do {
+                            e = entry_of(a, ++entry);
+                            m = parts_of(a, e);
+                        } while (m == 0);
+                    }
+                }
             }
         }
     }
