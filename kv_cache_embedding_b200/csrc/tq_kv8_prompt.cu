@@ -41,6 +41,7 @@ using sc::ffma2;
 namespace {
 
 constexpr int kPT = 128;            // keys a tile
+constexpr int kPH = 64;             // keys a half of a tile: what a stage works on at a time
 constexpr int kPM = 128;            // rows a stage
 constexpr int kPRows = 2 * kPM;     // rows an item
 constexpr int kPThreads = 512;
@@ -70,7 +71,7 @@ struct PSmem {
     uint32_t absent[kRing];       // 16-key groups without a page
     Work work[kWorks];
     uint64_t raw_full[2], raw_empty[2], kv_full[4], kv_empty[4];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], mma_done;
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [stage][half]
     uint64_t work_full[kWorks], work_empty[kWorks];
     uint32_t tmem_base;
     int abort;
@@ -142,15 +143,6 @@ __device__ __forceinline__ float2 exp2_pair(float2 x) {
                        __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
-template <int N>
-__device__ __forceinline__ void regs_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 template <int FMT, int D, typename T>
 __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                                                               const __grid_constant__ CUtensorMap kmap,
@@ -188,9 +180,11 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 mbar_init(&sm.raw_full[i], 1);
                 mbar_init(&sm.raw_empty[i], 4);
                 mbar_init(&sm.q_full[i], 4);
-                mbar_init(&sm.s_full[i], 1);
-                mbar_init(&sm.p_full[i], 4);
-                mbar_init(&sm.o_full[i], 1);
+                for (int h = 0; h < 2; ++h) {
+                    mbar_init(&sm.s_full[i][h], 1);
+                    mbar_init(&sm.p_full[i][h], 4);
+                    mbar_init(&sm.o_done[i][h], 1);
+                }
             }
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&sm.kv_full[i], 4);
@@ -265,11 +259,10 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
 
     if (warp < 8) {
         // ================================================== softmax, a row a thread
-        regs_up<192>();
         const int st = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t s_col = lane_addr + st * kPT, o_col = lane_addr + 2 * kPT + st * D;
-        uint32_t tile = 0, n_s = 0, n_o = 0;  // tiles so far; waits on s_full, o_full
+        const uint32_t o_col = lane_addr + 2 * kPT + st * D;
+        uint32_t tile = 0, halves = 0;  // tiles so far; halves of tiles that this stage has seen
         bool ok = true;
         for (uint32_t n = 0; ok && (ok = get(n)); ++n) {
             const Work& w = sm.work[n % kWorks];
@@ -324,28 +317,29 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             const int low = valid ? below_window(a, pos) : -1;
             float m = -INFINITY;
             float2 L2 = make_float2(0.f, 0.f);
-            for (int t = t_begin, key0 = (w.t0 + t_begin) * kPT; t < t_end; ++t, ++tile, key0 += kPT) {
-                const int rg = tile & (kRing - 1);
-                if (!wait(&sm.s_full[st], n_s & 1)) {
+            const uint32_t first = halves, last = halves + 2 * (t_end - t_begin);
+            for (int key0 = (w.t0 + t_begin) * kPT; halves < last; key0 += kPH) {
+                const int h = halves & 1, rg = (tile + ((halves - first) >> 1)) & (kRing - 1);
+                const uint32_t s_col = lane_addr + st * kPT + h * kPH;
+                if (!wait(&sm.s_full[st][h], halves >> 1 & 1)) {
                     ok = false;
                     break;
                 }
-                ++n_s;
                 tc_fence_after();
-                uint32_t s[4][32];
+                uint32_t s[2][32];
                 tmem_ld32(s_col, s[0]);
-                float cg[kGroups];
+                float cg[4];
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) cg[g] = sl * sm.kscale[rg][g];
-                const uint32_t absent = sm.absent[rg];
-                const bool masked = __any_sync(0xffffffffu, key0 + kPT - 1 > lim || key0 <= low || absent);
+                for (int g = 0; g < 4; ++g) cg[g] = sl * sm.kscale[rg][4 * h + g];
+                const uint32_t absent = sm.absent[rg] >> 4 * h & 15u;
+                const bool masked = __any_sync(0xffffffffu, key0 + kPH - 1 > lim || key0 <= low || absent);
                 float top = -INFINITY;
                 // 32 keys are on their way while the 32 before them are looked at
                 if (masked) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         tmem_wait_ld();
-                        if (c < 3) tmem_ld32(s_col + 32 * (c + 1), s[c + 1]);
+                        if (c < 1) tmem_ld32(s_col + 32, s[1]);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const int key = key0 + 32 * c + i;
@@ -356,12 +350,12 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         }
                     }
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) cg[g] = 1.f;
+                    for (int g = 0; g < 4; ++g) cg[g] = 1.f;
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         tmem_wait_ld();
-                        if (c < 3) tmem_ld32(s_col + 32 * (c + 1), s[c + 1]);
+                        if (c < 1) tmem_ld32(s_col + 32, s[1]);
                         const float x0 = max16(&s[c][0]) * cg[2 * c], x1 = max16(&s[c][16]) * cg[2 * c + 1];
                         top = max3(top, x0, x1);
                     }
@@ -375,8 +369,13 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     L2.x *= shrink;
                     L2.y *= shrink;
                 }
-                if (t > t_begin && __any_sync(0xffffffffu, grow)) {
-                    // S of this tile is complete, so O += P V of the last one is too
+                if (halves > first && __any_sync(0xffffffffu, grow)) {
+                    // O holds all halves before this one when the last one's MMAs are done
+                    if (!wait(&sm.o_done[st][(halves - 1) & 1], ((halves - 1) >> 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
@@ -390,18 +389,18 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 const float base = m == -INFINITY ? 0.f : -m;
                 auto probabilities = [&](auto some) {  // some: pairs of 8 that go to the polynomial
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t p[16];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int g = 2 * c + h;
-                            const float vw = sm.vscale[rg][g];
+                        for (int k = 0; k < 2; ++k) {
+                            const int g = 2 * c + k;
+                            const float vw = sm.vscale[rg][4 * h + g];
                             const float2 cc = make_float2(cg[g], cg[g]), bb = make_float2(base, base);
                             const float2 ww = make_float2(vw, vw);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                float2 x = make_float2(__uint_as_float(s[c][16 * h + 2 * i]),
-                                                       __uint_as_float(s[c][16 * h + 2 * i + 1]));
+                                float2 x = make_float2(__uint_as_float(s[c][16 * k + 2 * i]),
+                                                       __uint_as_float(s[c][16 * k + 2 * i + 1]));
                                 x = ffma2(x, cc, bb);
                                 if (i % 4 < some / 2) {
                                     x = exp2_pair(x);
@@ -411,7 +410,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                                 }
                                 L2 = __fadd2_rn(L2, x);
                                 x = __fmul2_rn(x, ww);
-                                p[8 * h + i] = half2_bits(x.x, x.y);
+                                p[8 * k + i] = half2_bits(x.x, x.y);
                             }
                         }
                         tmem_st16(s_col + 16 * c, p);
@@ -422,14 +421,12 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[st]);
+                if (lane == 0) mbar_arrive(&sm.p_full[st][h]);
+                ++halves;
             }
+            tile += t_end - t_begin;
+            for (int h = 0; h < 2; ++h) ok = ok && wait(&sm.o_done[st][h], ((halves - 1) >> 1) & 1);
             if (!ok) break;
-            if (!wait(&sm.o_full[st], n_o & 1)) {
-                ok = false;
-                break;
-            }
-            ++n_o;
             tc_fence_after();
             const float L = L2.x + L2.y;
             const bool begins = t_begin == 0, ends = t_end == w.nt;
@@ -485,7 +482,6 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             done_with(n);
         }
     } else {
-        regs_down<64>();
         if (warp < 12) {
             // ============================================== codes -> halves
             const int tid = threadIdx.x - 256;
@@ -569,30 +565,33 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             }
         } else if (warp == 12) {
             // ============================================== MMAs
-            constexpr uint32_t kQK = idesc_f16(0, kPM, kPT);
+            constexpr uint32_t kQK = idesc_f16(0, kPM, kPH);
             constexpr uint32_t kPV = idesc_f16(0, kPM, D) | (1u << 16);  // B MN-major
             const uint32_t qb = smem_u32(sm.q[0]), kvb = smem_u32(sm.kv[0]);
             constexpr uint32_t kQBytes = kPM * D * 2;
-            uint32_t tile = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+            uint32_t tile = 0, n_q[2] = {0, 0}, n_t[2] = {0, 0};  // items, tiles of a stage
             bool ok = true;
-            auto qk = [&](int st, uint32_t u) {  // S of tile u
-                if (lane == 0) {
+            // (an offset within an operand adds to its descriptor, in units of 16 bytes)
+            auto qk = [&](int st, uint32_t u, int h) {  // S of half h of tile u
+                const uint64_t q = smem_desc_kmajor_sw128(qb + st * kQBytes);
+                const uint64_t kd = smem_desc_kmajor_sw128(kvb + (u & 1) * kQBytes + h * kPH * 128);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k >> 2) * kBlock + (k & 3) * 32;
-                        mma_f16_ss(tbase + st * kPT, smem_desc_kmajor_sw128(qb + st * kQBytes + off),
-                                   smem_desc_kmajor_sw128(kvb + (u & 1) * kQBytes + off), kQK, k > 0);
+                        const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) / 16;
+                        mma_f16_ss(tbase + st * kPT + h * kPH, q + off, kd + off, kQK, k > 0);
                     }
-                    tc_commit(&sm.s_full[st]);
+                    tc_commit(&sm.s_full[st][h]);
                 }
             };
-            auto pv = [&](int st, uint32_t u, bool first) {
-                if (lane == 0) {
+            auto pv = [&](int st, uint32_t u, int h, bool first) {
+                const uint64_t v = smem_desc_mnmajor_sw128(kvb + (2 + (u & 1)) * kQBytes + h * kPH * 128, kBlock);
+                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kPT / 16; ++k)
-                        mma_f16_ts(tbase + 2 * kPT + st * D, tbase + st * kPT + 8 * k,
-                                   smem_desc_mnmajor_sw128(kvb + (2 + (u & 1)) * kQBytes + k * 2048, kBlock),
+                    for (int k = 0; k < kPH / 16; ++k)
+                        mma_f16_ts(tbase + 2 * kPT + st * D, tbase + st * kPT + h * kPH + 8 * k, v + k * 2048 / 16,
                                    kPV, !(first && k == 0));
+                    tc_commit(&sm.o_done[st][h]);
                 }
             };
             for (uint32_t n = 0; ok && (ok = get(n)); ++n) {
@@ -607,34 +606,35 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 if (ok) ok = wait(&sm.kv_full[tile & 1], (tile >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                for (int st = 0; st < nst; ++st) qk(st, tile);
-                if (lane == 0) tc_commit(&sm.kv_empty[tile & 1]);
+                for (int h = 0; h < 2; ++h)
+                    for (int st = 0; st < nst; ++st) qk(st, tile, h);
+                if (elect_one()) tc_commit(&sm.kv_empty[tile & 1]);
+                // S of a half is two halves ahead of P V: its stage never waits for it
                 for (int t = 0; t < tiles && ok; ++t, ++tile) {
                     const bool more = t + 1 < tiles;
                     ok = wait(&sm.kv_full[2 + (tile & 1)], (tile >> 1) & 1);
-                    for (int st = 0; st < nst && ok; ++st) {
-                        ok = wait(&sm.p_full[st], n_p[st] & 1);
-                        ++n_p[st];
+                    for (int i = 0; i < 2 * nst && ok; ++i) {
+                        const int h = i >= nst, st = i - h * nst;
+                        ok = wait(&sm.p_full[st][h], n_t[st] & 1);
+                        n_t[st] += h;
                         if (!ok) break;
                         tc_fence_after();
-                        pv(st, tile, t == 0);
-                        if (more && st == 0) ok = wait(&sm.kv_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
-                        if (!ok) break;
-                        if (more) qk(st, tile + 1);
-                        else if (lane == 0) tc_commit(&sm.o_full[st]);
+                        pv(st, tile, h, t == 0 && h == 0);
+                        if (!more) continue;
+                        if (i == 0) ok = wait(&sm.kv_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
+                        if (ok) qk(st, tile + 1, h);
                     }
-                    if (ok && lane == 0) {
+                    if (ok && elect_one()) {
                         tc_commit(&sm.kv_empty[2 + (tile & 1)]);
                         if (more) tc_commit(&sm.kv_empty[(tile + 1) & 1]);
                     }
                 }
             }
             // all MMAs are done before tensor and shared memory go
-            if (lane == 0) {
-                tc_commit(&sm.mma_done);
-                int none = 0;
-                mbar_wait(&sm.mma_done, 0, &none, kWaitNs);
-            }
+            if (elect_one()) tc_commit(&sm.mma_done);
+            __syncwarp();
+            int none = 0;
+            mbar_wait(&sm.mma_done, 0, &none, kWaitNs);
             __syncwarp();
         } else if (warp == 13) {
             // ============================================== TMA
