@@ -13,22 +13,28 @@
 // evenly, contiguously, over one CTA an SM, so ragged and causal batches balance
 // and a long context with few rows fills the machine; the items that are cut are
 // joined by k_prompt_merge.  Warps:
-//   0-3, 4-7  softmax of stage 0, 1: a thread a row.  Loads its query row, turns
-//             S (tensor memory) into P in place, rescales O only when the row's
-//             maximum has grown by more than 2^8 (the reference m then follows;
-//             P <= 2^8 meanwhile, far inside a half's range), writes the result.
+//   0-3, 4-7  softmax of stage 0, 1: a thread a row, half a tile (64 keys) at a time.
+//             Loads its query row, turns S (tensor memory) into P in place, rescales
+//             O only when the row's maximum has grown by more than 2^8 (the reference
+//             m then follows; P <= 2^8 meanwhile, far inside a half's range), writes
+//             the result.
 //   8-11      codes -> halves: from the TMA ring (128 keys x d bytes) into the
 //             swizzled operand tiles of K (K-major) and V (the same rows, read
 //             MN-major), with the tile's scales.
-//   12        issues the MMAs: per tile and stage O += P V of this tile, then S of
-//             the next, so each stage's softmax hides behind the other's MMAs.
+//   12, 15    issue the MMAs of stage 0, 1: per half O += P V, then S of the half
+//             two further, so the softmax finds its next S complete.
 //   13        the TMA loads, a page table lookup a box, a tile ahead.
 //   14        walks the CTA's share and hands the others its items, with R, through
 //             a short ring: lengths, divisions and lookups are off their path.
 // Every wait is bounded (1 s); a warp that gives up sets the abort flag and the
 // call's status.
-#include <type_traits>
-
+//
+// Measured (4096 tokens x 32 heads of 128 over 16384 keys, causal): 1040 us, 925
+// TFLOP/s.  The softmax bounds it: 64 keys take a stage 2100 cycles against 600
+// of MMAs, by issue slots (some 5 instructions an element of S, shared with the
+// conversion's) and the latency of its chain.  Tried and slower: a quarter or half
+// of the exponentials as polynomials on the FMA pipe (1087, 1181 us), whole tiles
+// (1101 us), one warp for both stages' MMAs (1189 us).
 #include "tq_kv8_attention.cuh"
 #include "tq_score_common.cuh"
 
@@ -71,7 +77,7 @@ struct PSmem {
     uint32_t absent[kRing];       // 16-key groups without a page
     Work work[kWorks];
     uint64_t raw_full[2], raw_empty[2], kv_full[4], kv_empty[4];
-    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], mma_done;  // [stage][half]
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2], mma_done[2];  // [stage][half]
     uint64_t work_full[kWorks], work_empty[kWorks];
     uint32_t tmem_base;
     int abort;
@@ -124,25 +130,6 @@ __device__ __forceinline__ float max16(const uint32_t* s) {
     return max3(max3(a, f(10), f(11)), max3(b, f(12), f(13)), fmaxf(f(14), f(15)));
 }
 
-// 2^x for x <= 126 on the FMA pipe (below -126: 2^-126): x = n + f with |f| <= 1/2,
-// 2^f by the degree-5 Chebyshev expansion (within 2^-23), n into the exponent.  The
-// exponential unit alone (16 a clock) would take as long as the MMAs of a tile.
-constexpr int kPoly = 2;  // of 8 pairs
-__device__ __forceinline__ float2 exp2_pair(float2 x) {
-    auto both = [](float v) { return make_float2(v, v); };
-    x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
-    const float2 t = __fadd2_rn(x, both(12582912.f));  // n in the last bits
-    const float2 n = __fadd2_rn(t, both(-12582912.f));
-    const float2 f = ffma2(n, both(-1.f), x);
-    float2 p = ffma2(f, both(0.0013427354f), both(0.009673781f));
-    p = ffma2(p, f, both(0.05550341f));
-    p = ffma2(p, f, both(0.24022229f));
-    p = ffma2(p, f, both(0.6931472f));
-    p = ffma2(p, f, both(1.f));
-    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-}
-
 template <int FMT, int D, typename T>
 __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                                                               const __grid_constant__ CUtensorMap kmap,
@@ -188,13 +175,14 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             }
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&sm.kv_full[i], 4);
-                mbar_init(&sm.kv_empty[i], 1);
+                mbar_init(&sm.kv_empty[i], 2);
             }
             for (int i = 0; i < kWorks; ++i) {
                 mbar_init(&sm.work_full[i], 1);
-                mbar_init(&sm.work_empty[i], 14);  // all warps but the scheduler's own and the idle one
+                mbar_init(&sm.work_empty[i], 15);  // all warps but the one that fills it
             }
-            mbar_init(&sm.mma_done, 1);
+            mbar_init(&sm.mma_done[0], 1);
+            mbar_init(&sm.mma_done[1], 1);
             fence_mbar_init();
             prefetch_tmap(&kmap);
             prefetch_tmap(&vmap);
@@ -387,37 +375,29 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     }
                 }
                 const float base = m == -INFINITY ? 0.f : -m;
-                auto probabilities = [&](auto some) {  // some: pairs of 8 that go to the polynomial
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t p[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t p[16];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int g = 2 * c + k;
-                            const float vw = sm.vscale[rg][4 * h + g];
-                            const float2 cc = make_float2(cg[g], cg[g]), bb = make_float2(base, base);
-                            const float2 ww = make_float2(vw, vw);
+                    for (int k = 0; k < 2; ++k) {
+                        const int g = 2 * c + k;
+                        const float vw = sm.vscale[rg][4 * h + g];
+                        const float2 cc = make_float2(cg[g], cg[g]), bb = make_float2(base, base);
+                        const float2 ww = make_float2(vw, vw);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float2 x = make_float2(__uint_as_float(s[c][16 * k + 2 * i]),
-                                                       __uint_as_float(s[c][16 * k + 2 * i + 1]));
-                                x = ffma2(x, cc, bb);
-                                if (i % 4 < some / 2) {
-                                    x = exp2_pair(x);
-                                } else {
-                                    x.x = ex2(x.x);
-                                    x.y = ex2(x.y);
-                                }
-                                L2 = __fadd2_rn(L2, x);
-                                x = __fmul2_rn(x, ww);
-                                p[8 * k + i] = half2_bits(x.x, x.y);
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            float2 x = make_float2(__uint_as_float(s[c][16 * k + 2 * i]),
+                                                   __uint_as_float(s[c][16 * k + 2 * i + 1]));
+                            x = ffma2(x, cc, bb);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            L2 = __fadd2_rn(L2, x);
+                            x = __fmul2_rn(x, ww);
+                            p[8 * k + i] = half2_bits(x.x, x.y);
                         }
-                        tmem_st16(s_col + 16 * c, p);
                     }
-                };
-                if (masked) probabilities(std::integral_constant<int, 0>{});
-                else probabilities(std::integral_constant<int, kPoly>{});
+                    tmem_st16(s_col + 16 * c, p);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -563,66 +543,69 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 }
                 done_with(n);
             }
-        } else if (warp == 12) {
-            // ============================================== MMAs
+        } else if (warp == 12 || warp == 15) {
+            // ============================================== MMAs of a stage
+            const int st = warp == 15;
             constexpr uint32_t kQK = idesc_f16(0, kPM, kPH);
             constexpr uint32_t kPV = idesc_f16(0, kPM, D) | (1u << 16);  // B MN-major
-            const uint32_t qb = smem_u32(sm.q[0]), kvb = smem_u32(sm.kv[0]);
             constexpr uint32_t kQBytes = kPM * D * 2;
-            uint32_t tile = 0, n_q[2] = {0, 0}, n_t[2] = {0, 0};  // items, tiles of a stage
+            const uint32_t qb = smem_u32(sm.q[st]), kvb = smem_u32(sm.kv[0]);
+            const uint32_t s_col = tbase + st * kPT, o_col = tbase + 2 * kPT + st * D;
+            uint32_t tile = 0, n_q = 0, n_t = 0;  // all tiles; items and tiles of the stage
             bool ok = true;
             // (an offset within an operand adds to its descriptor, in units of 16 bytes)
-            auto qk = [&](int st, uint32_t u, int h) {  // S of half h of tile u
-                const uint64_t q = smem_desc_kmajor_sw128(qb + st * kQBytes);
+            auto qk = [&](uint32_t u, int h) {  // S of half h of tile u
+                const uint64_t q = smem_desc_kmajor_sw128(qb);
                 const uint64_t kd = smem_desc_kmajor_sw128(kvb + (u & 1) * kQBytes + h * kPH * 128);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) / 16;
-                        mma_f16_ss(tbase + st * kPT + h * kPH, q + off, kd + off, kQK, k > 0);
+                        mma_f16_ss(s_col + h * kPH, q + off, kd + off, kQK, k > 0);
                     }
                     tc_commit(&sm.s_full[st][h]);
                 }
             };
-            auto pv = [&](int st, uint32_t u, int h, bool first) {
+            auto pv = [&](uint32_t u, int h, bool first) {
                 const uint64_t v = smem_desc_mnmajor_sw128(kvb + (2 + (u & 1)) * kQBytes + h * kPH * 128, kBlock);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kPH / 16; ++k)
-                        mma_f16_ts(tbase + 2 * kPT + st * D, tbase + st * kPT + h * kPH + 8 * k, v + k * 2048 / 16,
-                                   kPV, !(first && k == 0));
+                        mma_f16_ts(o_col, s_col + h * kPH + 8 * k, v + k * 2048 / 16, kPV, !(first && k == 0));
                     tc_commit(&sm.o_done[st][h]);
                 }
             };
             for (uint32_t n = 0; ok && (ok = get(n)); ++n) {
                 const Work& w = sm.work[n % kWorks];
-                const int nst = w.rows > kPM ? 2 : 1, tiles = w.t_end - w.t;
-                if (w.rows == 0) break;
+                const int tiles = w.t_end - w.t, rows = w.rows;
+                if (rows == 0) break;
                 done_with(n);
-                for (int st = 0; st < nst && ok; ++st) {
-                    ok = wait(&sm.q_full[st], n_q[st] & 1);
-                    ++n_q[st];
+                if (st * kPM >= rows) {  // not for this stage: its consent to every tile's release
+                    for (int t = 0; t < tiles && ok; ++t, ++tile)
+                        for (uint32_t b = tile & 1; b < 4 && ok; b += 2) {
+                            ok = wait(&sm.kv_full[b], (tile >> 1) & 1);
+                            if (ok && lane == 0) mbar_arrive(&sm.kv_empty[b]);
+                        }
+                    continue;
                 }
-                if (ok) ok = wait(&sm.kv_full[tile & 1], (tile >> 1) & 1);
+                ok = wait(&sm.q_full[st], n_q++ & 1) && wait(&sm.kv_full[tile & 1], (tile >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                for (int h = 0; h < 2; ++h)
-                    for (int st = 0; st < nst; ++st) qk(st, tile, h);
+                qk(tile, 0);
+                qk(tile, 1);
                 if (elect_one()) tc_commit(&sm.kv_empty[tile & 1]);
-                // S of a half is two halves ahead of P V: its stage never waits for it
-                for (int t = 0; t < tiles && ok; ++t, ++tile) {
+                // S of a half is two halves ahead of P V: its softmax never waits for it
+                for (int t = 0; t < tiles && ok; ++t, ++tile, ++n_t) {
                     const bool more = t + 1 < tiles;
                     ok = wait(&sm.kv_full[2 + (tile & 1)], (tile >> 1) & 1);
-                    for (int i = 0; i < 2 * nst && ok; ++i) {
-                        const int h = i >= nst, st = i - h * nst;
-                        ok = wait(&sm.p_full[st][h], n_t[st] & 1);
-                        n_t[st] += h;
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        ok = wait(&sm.p_full[st][h], n_t & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        pv(st, tile, h, t == 0 && h == 0);
+                        pv(tile, h, t == 0 && h == 0);
                         if (!more) continue;
-                        if (i == 0) ok = wait(&sm.kv_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
-                        if (ok) qk(st, tile + 1, h);
+                        if (h == 0) ok = wait(&sm.kv_full[(tile + 1) & 1], ((tile + 1) >> 1) & 1);
+                        if (ok) qk(tile + 1, h);
                     }
                     if (ok && elect_one()) {
                         tc_commit(&sm.kv_empty[2 + (tile & 1)]);
@@ -631,10 +614,10 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 }
             }
             // all MMAs are done before tensor and shared memory go
-            if (elect_one()) tc_commit(&sm.mma_done);
+            if (elect_one()) tc_commit(&sm.mma_done[st]);
             __syncwarp();
             int none = 0;
-            mbar_wait(&sm.mma_done, 0, &none, kWaitNs);
+            mbar_wait(&sm.mma_done[st], 0, &none, kWaitNs);
             __syncwarp();
         } else if (warp == 13) {
             // ============================================== TMA
