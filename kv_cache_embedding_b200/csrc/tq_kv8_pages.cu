@@ -84,15 +84,35 @@ __device__ __forceinline__ int pages_for(const View& v, int64_t tokens) {
     return (int)((tokens + v.page - 1) >> v.page_log2);
 }
 
-// Whether a slot is twice in the list (marks: one word a slot, any contents).
-// Ends with a barrier.
-__device__ __forceinline__ bool repeated(const View& v, const int32_t* slots, int n, int32_t* marks) {
-    for (int i = threadIdx.x; i < n; i += kPT)
-        if ((unsigned)slots[i] < (unsigned)v.slots) marks[slots[i]] = 0;
-    __syncthreads();
+// Whether a slot is twice in the list, or one of `others` (may be null) is in it.
+// Short lists are compared entry by entry in shared memory; a long one is counted
+// in the workspace (marks: one word a slot, any contents).  Ends with a barrier.
+constexpr int kShortList = 256;
+__device__ __forceinline__ bool repeated(const View& v, const int32_t* slots, const int32_t* others, int n,
+                                         int32_t* marks) {
+    __shared__ int32_t s_list[kShortList];
     bool bad = false;
+    if (n <= kShortList) {
+        const int i = threadIdx.x % kShortList;
+        if ((int)threadIdx.x < n) s_list[i] = slots[i];
+        const int other = others && i < n ? others[i] : 0;
+        __syncthreads();
+        if (i < n)
+            for (int j = threadIdx.x / kShortList; j < n; j += kPT / kShortList)
+                bad |= (j != i && s_list[j] == s_list[i]) || (others && s_list[j] == other);
+        return __syncthreads_or(bad) != 0;
+    }
+    for (int i = threadIdx.x; i < n; i += kPT) {
+        if ((unsigned)slots[i] < (unsigned)v.slots) marks[slots[i]] = 0;
+        if (others && (unsigned)others[i] < (unsigned)v.slots) marks[others[i]] = 0;
+    }
+    __syncthreads();
     for (int i = threadIdx.x; i < n; i += kPT)
         if ((unsigned)slots[i] < (unsigned)v.slots) bad |= atomicAdd(&marks[slots[i]], 1) != 0;
+    __syncthreads();
+    if (others)
+        for (int i = threadIdx.x; i < n; i += kPT)
+            if ((unsigned)others[i] < (unsigned)v.slots) bad |= marks[others[i]] != 0;
     return __syncthreads_or(bad) != 0;
 }
 
@@ -104,16 +124,17 @@ __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t
     __shared__ int32_t s_held[kMaxList];  // the shared page that entry i writes into, or -1
     __shared__ int32_t s_base[kMaxList];  // first of the entry's new pages
     grid_begin();
-    bool bad = repeated(v, slots, n, w.marks);
+    const int per = (n + kPT - 1) / kPT;  // entries of a thread
+    bool bad = repeated(v, slots, nullptr, n, w.marks);
     if (threadIdx.x == 0) w.head[1] = 0;
     int at[kPer], more[kPer], need[kPer];
     bool shared_page = false;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-        const int i = threadIdx.x * kPer + e;  // neighbours: list order is thread order
+        const int i = threadIdx.x * per + e;  // neighbours: list order is thread order
         at[e] = more[e] = need[e] = 0;
         int held = -1;
-        if (i < n) {
+        if (e < per && i < n) {
             const int s = slots[i], add = counts[i];
             if ((unsigned)s >= (unsigned)v.slots || add < 0) {
                 bad = true;
@@ -129,15 +150,15 @@ __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t
                 }
             }
         }
-        if (i < kMaxList) s_held[i] = held;
+        if (e < per && i < n) s_held[i] = held;
     }
     // an entry copies unless the entries before it leave it the last holder
     unsigned copy = 0;
     if (__syncthreads_or(shared_page)) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const int i = threadIdx.x * kPer + e;
-            if (i < n && s_held[i] >= 0) {
+            const int i = threadIdx.x * per + e;
+            if (e < per && i < n && s_held[i] >= 0) {
                 int before = 0;
                 for (int j = 0; j < i; ++j) before += s_held[j] == s_held[i];
                 if (refs[s_held[i]] - before > 1) {
@@ -185,8 +206,8 @@ __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t
     int64_t b = base, ci = cbase;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-        const int i = threadIdx.x * kPer + e;
-        if (i < n) {
+        const int i = threadIdx.x * per + e;
+        if (e < per && i < n) {
             const int s = slots[i];
             if (copy >> e & 1u) {
                 const int dst = w.ids[b], src = s_held[i];
@@ -214,8 +235,8 @@ __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-        const int i = threadIdx.x * kPer + e;
-        if (i < n) len[slots[i]] = at[e] + more[e];
+        const int i = threadIdx.x * per + e;
+        if (e < per && i < n) len[slots[i]] = at[e] + more[e];
     }
     if (threadIdx.x == 0) {
         w.head[0] = TQ_OK;
@@ -227,15 +248,11 @@ __global__ __launch_bounds__(kPT) void k_fork(View v, int32_t* table, int32_t* l
                                               int n, const int32_t* parents,
                                               const int32_t* children, PagesWs w) {
     grid_begin();
-    // marks: parents cleared first, then the children counted
-    for (int i = threadIdx.x; i < n; i += kPT)
-        if ((unsigned)parents[i] < (unsigned)v.slots) w.marks[parents[i]] = 0;
-    __syncthreads();
-    bool bad = repeated(v, children, n, w.marks);
+    bool bad = repeated(v, children, parents, n, w.marks);
     for (int i = threadIdx.x; i < n; i += kPT) {
         const int p = parents[i], c = children[i];
         if ((unsigned)p >= (unsigned)v.slots || (unsigned)c >= (unsigned)v.slots) bad = true;
-        else bad |= w.marks[p] != 0 || len[c] != 0;
+        else bad |= len[c] != 0;
     }
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) w.head[0] = TQ_ERR_ARG;
@@ -258,7 +275,7 @@ __global__ __launch_bounds__(kPT) void k_truncate(View v, int32_t* table, int32_
                                                   const int32_t* slots,
                                                   const int32_t* lens, PagesWs w) {
     grid_begin();
-    bool bad = repeated(v, slots, n, w.marks);
+    bool bad = repeated(v, slots, nullptr, n, w.marks);
     for (int i = threadIdx.x; i < n; i += kPT)
         bad |= (unsigned)slots[i] >= (unsigned)v.slots || lens[i] < 0;
     if (__syncthreads_or(bad)) {

@@ -735,6 +735,33 @@ def test_pages_device_refusals(tq_lib, cuda):
     assert (c.refs == 1).all()
 
 
+@pytest.mark.parametrize("n", [255, 256, 257, 1025, 3000])
+def test_pages_list_lengths(tq_lib, cuda, n):
+    """Lists around the lengths at which the checks change their way: the plain
+    rules, copies on write of one page by many, and a repeated slot at either end."""
+    c = make_cache(tq_lib, cuda, "i8", layers=1, heads=1, d=64, page=16, slots=n + 2, max_pages=3,
+                   pages=2 * n + 8)
+    m = Model(n + 2, 3, 2 * n + 8, 16)
+
+    def both(kind, a, b, what="OK"):
+        got = getattr(m, kind)(a, b) if what == "OK" else what
+        assert (got[0] if isinstance(got, tuple) else got) == what
+        getattr(c, kind)(ints(a, cuda), ints(b, cuda))
+        expect(tq_lib, c, what)
+        m.same(c)
+    both("reserve", [n, n + 1], [20, 7])
+    kids = list(range(n))
+    both("fork", [n if i % 3 else n + 1 for i in kids], kids)
+    both("reserve", kids[::-1], [i % 5 for i in kids])
+    for bad in (kids[:-1] + [0], [kids[-1]] + kids[1:]):
+        both("truncate", bad, [0] * n, "ARG")
+        both("reserve", bad, [1] * n, "ARG")
+    both("truncate", kids, [0] * n)
+    both("fork", [n] * (n - 1) + [0], kids, "ARG")   # a parent among the children
+    both("fork", [n] * n, kids[:-1] + [0], "ARG")
+    both("fork", [n] * n, kids)
+
+
 # ------------------------------------------------------------------ together
 
 def test_engine_steps(tq_lib, cuda):
