@@ -409,7 +409,7 @@ TQ_API int tq_rope(const tq_rope_params_t *r, int64_t T, int heads, const void *
  * A slot is a sequence: a row of the table and a length in tokens; token j of a
  * slot lies in page table[j / page] at row j % page.  A page belongs to all
  * layers at once.  refs counts the slots that hold a page (0: free).  A key or
- * value is scale * code; rows of a page that no token was written to may hold
+ * value is scale * code (scale >= 0); rows of a page that no token was written to may hold
  * any bytes (none of the calls below reads them into a result).
  * Limits: d 64 or 128; page 16, 32, 64 or 128; heads, layers, slots,
  * max_pages, pages >= 1; pages * heads * page < 2^31; d_k and d_v 16-byte
@@ -505,7 +505,8 @@ TQ_API int tq_kv8_read(const tq_kv8_t *c, int layer, int ns, const int32_t *d_sl
  * d_q, d_out: [total_q][heads_q][d] of q_dtype (TQ_BF16 or TQ_F16); q with
  * strides in elements (multiples of 8, the base 16-byte aligned), out
  * contiguous.  d_lse: [total_q][heads_q] fp32 or NULL.  heads_q a multiple of
- * heads, at most 128 times as many (else TQ_ERR_UNSUPPORTED).
+ * heads, at most 128 times as many, total_q times that multiple below 2^31 - 2^16
+ * (else TQ_ERR_UNSUPPORTED).
  * d_ws: >= tq_kv8_workspace_bytes(TQ_KV8_OP_ATTENTION, c, ns, total_q, max_q,
  * heads_q), any contents; calls that overlap on the GPU need workspaces of their
  * own.  The result does not depend on what else runs, nor on earlier calls.  A

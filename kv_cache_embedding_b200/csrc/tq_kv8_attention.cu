@@ -19,6 +19,11 @@
 // 8 rows cost half of what 16 do.  Fragments are made in registers from the codes
 // (K: plain ldmatrix, coordinates permuted alike on both sides; V: transposing
 // ldmatrix of byte pairs, the halves sorted out by byte permutes).
+//
+// Measured: 4 x 131072 keys x 8 heads of 128, one token of 32 heads: 187 us, 5.7 TB/s
+// (a copy runs at 6.55); 64 ragged sequences 104 us, 5.3 TB/s; one sequence of 500
+// keys 9 us, a chain of lookups, two tiles of dependent instructions and the join.
+// With 8 warps of 16 rows and lookups in line: 233, 122 and 10.4 us.
 #include <atomic>
 #include <chrono>
 #include <cmath>
@@ -899,7 +904,7 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
     if (!d_slots && ns > c->slots) return TQ_ERR_ARG;
     if (heads_q % c->heads || heads_q / c->heads > 128) return TQ_ERR_UNSUPPORTED;
     // rows (tokens x group) count in 32 bits
-    if (total_q >= ((int64_t)1 << 31) / (heads_q / c->heads) - 512) return TQ_ERR_UNSUPPORTED;
+    if (total_q > (((int64_t)1 << 31) - (1 << 16)) / (heads_q / c->heads)) return TQ_ERR_UNSUPPORTED;
     if (ns == 0 || total_q == 0 || max_q == 0) return TQ_OK;
     if (!d_cu || !d_q || !d_out || (((uintptr_t)d_q | (uintptr_t)d_out) & 15u) || q_ts % 8 || q_hs % 8)
         return TQ_ERR_ARG;

@@ -18,15 +18,17 @@ _SCALINGS = {"none": B.TQ_ROPE_PLAIN, "linear": B.TQ_ROPE_LINEAR, "ntk": B.TQ_RO
 
 
 class _RopeFn(torch.autograd.Function):
+    """A linear map: its gradient is the transposed one, again with a gradient."""
+
     @staticmethod
-    def forward(ctx, x, pos, rope):
-        ctx.rope = rope
+    def forward(ctx, x, pos, rope, transpose):
+        ctx.rope, ctx.transpose = rope, transpose
         ctx.save_for_backward(pos)
-        return rope.apply(x, pos)
+        return rope.apply(x, pos, transpose=transpose)
 
     @staticmethod
     def backward(ctx, g):
-        return ctx.rope.apply(g, ctx.saved_tensors[0], transpose=True), None, None
+        return _RopeFn.apply(g, ctx.saved_tensors[0], ctx.rope, not ctx.transpose), None, None, None
 
 
 class Rope:
@@ -55,7 +57,7 @@ class Rope:
 
     def __call__(self, x, pos):
         """apply(x, pos) with a gradient."""
-        return _RopeFn.apply(x, pos, self)
+        return _RopeFn.apply(x, pos, self, False)
 
 
 class KV8Cache:

@@ -126,6 +126,23 @@ def test_rope_gradient(tq_lib, cuda, layout):
         assert abs(float(d) - float(x.grad[t, h, i])) <= 2.0 ** -13
 
 
+def test_rope_second_gradient(tq_lib, cuda):
+    """The gradient of a squared gradient: g = R^T (w (R x)) with elementwise w, so
+    d(sum g u)/dx = R^T (w (R u)), by the map's own forms."""
+    g = gen(10)
+    r = tq_lib.Rope(64, 64, layout="half")
+    x, u, w = (torch.randn(3, 2, 64, generator=g).to(cuda) for _ in range(3))
+    x.requires_grad_()
+    pos = torch.tensor([3, 77, 5000], device=cuda)
+    y = r(x, pos)
+    first, = torch.autograd.grad((0.5 * w * y * y).sum(), x, create_graph=True)
+    second, = torch.autograd.grad((first * u).sum(), x)
+    # each map is within 2^-21 of its largest terms (rope_bound); two maps of values
+    # up to 16 and a product: 16 x 2 x 2 x 2^-21
+    want = r.apply(w * r.apply(u, pos), pos, transpose=True)
+    assert ((second - want).abs() <= 2.0 ** -15).all()
+
+
 # ------------------------------------------------------------------ append and read
 
 def make_cache(tq_lib, dev, fmt="i8", layers=1, heads=2, d=128, page=64, slots=4, max_pages=8,
@@ -869,3 +886,34 @@ def test_calls_in_a_graph_and_on_other_streams(tq_lib, cuda):
         assert torch.equal(a.lens, b.lens) and torch.equal(a.table, b.table)
         ids = a.table[a.table >= 0].long()
         assert torch.equal(a.kscale[0, ids], b.kscale[0, ids])
+
+
+@pytest.mark.parametrize("counts", [[1, 1, 1], [3, 1, 2], [200, 1, 64]])
+def test_attention_replayed_and_side_by_side(tq_lib, cuda, counts):
+    """Items joined across blocks: a captured call replayed over changing queries,
+    on a side stream while eager calls run on others, gives what a call alone gives."""
+    lens = [30000, 5000, 700]
+    c = fill(tq_lib, cuda, "i8", 2, 128, 64, lens)
+    total = sum(counts)
+    cu, q = cu_of(counts, cuda), torch.zeros(total, 8, 128, dtype=torch.bfloat16, device=cuda)
+    qs = [torch.randn(total, 8, 128, generator=gen(i)).to(torch.bfloat16).to(cuda) for i in range(4)]
+    want = [c.attention(0, x, cu, max(counts)) for x in qs]
+    c.status()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = c.attention(0, q, cu, max(counts))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(12):
+        got = []
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if k == 0:
+                    q.copy_(qs[i % 4])
+                    g.replay()
+                else:
+                    got.append(((i + k) % 4, c.attention(0, qs[(i + k) % 4], cu, max(counts))))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i % 4]), i
+        assert all(torch.equal(x, want[j]) for j, x in got), i
+    c.status()

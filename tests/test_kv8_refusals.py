@@ -98,6 +98,15 @@ def test_token_calls(tq_lib):
     assert L.tq_kv8_workspace_bytes(B.TQ_KV8_OP_ATTENTION, c, 1, -1, 1, 4) == BIG
 
 
+def test_attention_row_count(tq_lib):
+    """Rows (tokens x group) count in 32 bits."""
+    B, L = tq_lib.binding, tq_lib.binding.lib
+    c = C.byref(_cache(B))
+    for heads_q, total in ((2, 1 << 31), (256, 1 << 24), (8, 1 << 29)):
+        assert L.tq_kv8_attention(c, 0, 1, None, 256, total, 1, heads_q, 256, B.TQ_BF16, 512, 128, 0.1, 1,
+                                  0, 256, None, 256, 1 << 60, None) == B.TQ_ERR_UNSUPPORTED
+
+
 def test_structs_match_the_header(tq_lib, tmp_path):
     import os
     import subprocess
