@@ -385,7 +385,7 @@ int read_type(const tq_kv8_t* c, int layer, int ns, const int32_t* slots, const 
               const int32_t* cu, int64_t total, int max_new, void* k, void* v, cudaStream_t s) {
     // a batch of items a thread, or fewer tokens a block where that leaves SMs idle
     const int per = c->heads * c->d / 16;
-    int64_t tokens = kReadItems * kReadThreads / per, fill = (int64_t)ns * max_new / (148 * 2);
+    int64_t tokens = kReadItems * kReadThreads / per, fill = (int64_t)ns * max_new / (148 * 4);
     if (tokens > fill) tokens = fill;
     tokens = tokens < 1 ? 1 : (tokens > max_new ? max_new : tokens);
     const int64_t bps = (max_new + tokens - 1) / tokens;

@@ -124,6 +124,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// Bits 0 .. n (none for n < 0).
+__device__ __forceinline__ uint32_t first_bits(int n) {
+    return n < 0 ? 0u : n >= 31 ? 0xFFFFFFFFu : (2u << n) - 1u;
+}
 __device__ __forceinline__ float max16(const uint32_t* s) {
     auto f = [&](int i) { return __uint_as_float(s[i]); };
     const float a = max3(max3(f(0), f(1), f(2)), f(3), f(4)), b = max3(max3(f(5), f(6), f(7)), f(8), f(9));
@@ -328,11 +332,12 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     for (int c = 0; c < 2; ++c) {
                         tmem_wait_ld();
                         if (c < 1) tmem_ld32(s_col + 32, s[1]);
+                        // the keys that the row sees, a bit each
+                        const uint32_t see = first_bits(lim - (key0 + 32 * c)) & ~first_bits(low - (key0 + 32 * c)) &
+                                             ~((absent >> 2 * c & 1u) * 0xFFFFu | (absent >> (2 * c + 1) & 1u) * 0xFFFF0000u);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const int key = key0 + 32 * c + i;
-                            const bool see = key <= lim && key > low && !(absent >> (2 * c + i / 16) & 1u);
-                            const float x = see ? __uint_as_float(s[c][i]) * cg[2 * c + i / 16] : -INFINITY;
+                            const float x = see >> i & 1u ? __uint_as_float(s[c][i]) * cg[2 * c + i / 16] : -INFINITY;
                             s[c][i] = __float_as_uint(x);
                             top = fmaxf(top, x);
                         }
