@@ -80,19 +80,20 @@ constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB of a warp's ring
 // block at work, so that they spread over the SMs.  "Unit" u is warp u % busy of
 // block u / busy.
 //
-// Joining.  Parts of an item that lies within a block meet in shared memory (the
-// ring of a warp that is through), or in the workspace where their warp goes on
-// with another item.  Of an item across blocks every part goes to the workspace
-// (part 2w: the end or middle of an item that warp w did not begin, 2w + 1 the
-// beginning of one), a block sets its flag behind the parts of the one item that
-// goes on beyond it, and the block in which the item ends waits for the flags of
-// the others -- blocks before it, which are dispatched before it -- and joins.  A
-// flag is set to the call's nonce and taken back by the joining block, so a
-// workspace needs no preparation and a replayed graph finds none set.  The order
-// of the sum is that of the keys.
+// Joining.  A block's parts of an item meet in shared memory (the ring of a warp
+// that is through), or in the workspace where their warp goes on with another item
+// (slot w of warp w of the grid).  Where the item lies within the block that is its
+// result; of an item across blocks each block leaves one sum in the workspace (slot
+// 2b: the end or middle of an item that block b did not begin, 2b + 1 the beginning
+// of one).  A block sets its flag behind its sum of the one item that goes on beyond
+// it, and the block in which the item ends waits for the flags of the others --
+// blocks before it, which are dispatched before it -- and joins.  A flag is set to
+// the call's nonce and taken back by the joining block, so a workspace needs no
+// preparation and a replayed graph finds none set.  The order of the sum is that of
+// the keys.
 //
-// Workspace: [status word (256 B) | a flag a block | per warp two parts: (m, L) of
-// 16 rows, 16 x d sums].
+// Workspace: [status word (256 B) | a flag a block | (m, L) of 16 rows and 16 x d
+// sums: a slot a warp, then two a block].
 struct Parts {
     int* status;
     uint64_t* flag;
@@ -101,12 +102,13 @@ struct Parts {
     uint64_t nonce;
 };
 
-// An item whose parts are to be joined.
+// A block's parts of an item.
 struct Job {
-    int64_t row0;   // its first row of the entry's (token x group) rows, from token 0
-    int64_t first;  // the unit that begins it
-    int parts;      // units that hold a part; 0: no job
+    int64_t row0;   // the item's first row of the entry's (token x group) rows, from token 0
+    int64_t first;  // the unit that begins the item
+    int parts;      // warps of the block that hold a part; 0: no job
     int rows, head;
+    bool begins, ends;  // in this block
 };
 
 template <int D>
@@ -124,8 +126,8 @@ struct Smem {
     int64_t warp_steps[kWarps];
     int warp_items[kWarps], warp_most[kWarps];
     float2 ml[kWarps][kRows];            // of the part that a warp leaves in its ring
-    Job own[kWarps], early;              // items within the block, by their first warp; begun before it
-    int outside[kWarps];                 // the end of an own item that this warp left in the workspace
+    Job job[kWarps + 1];                 // of the items that a warp begins; the last: begun before the block
+    int outside[kWarps];                 // this warp left the end of an item in the workspace
     int beyond;                          // an item goes on behind the block
     int abort;
 };
@@ -237,7 +239,7 @@ __device__ __forceinline__ Sum<D> sum_parts(int n, int i0, int step, int lane, M
 #pragma unroll
         for (int k = 0; k < E; ++k) s.acc[k] *= old;
         const int cnt = min(32, (n - c0 + step - 1) / step);
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < cnt; ++i) {
             const float* src = o(c0 + i * step) + lane * E;
             float y[E];
@@ -281,10 +283,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     if (threadIdx.x == 0) {
         sm.abort = 0;
         sm.beyond = 0;
-        sm.early.parts = 0;
     }
     if (lane == 0) {
-        sm.own[warp].parts = 0;
+        sm.job[warp].parts = 0;
+        sm.job[kWarps].parts = 0;
         sm.outside[warp] = 0;
     }
     if (lane < NS) mbar_init(&sm.full[warp][lane], 1);
@@ -395,6 +397,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             p.open(rem);
         }
     }
+    // a block's two sums lie behind the warps' slots
+    auto block_slot = [&](int b) { return (int64_t)gridDim.x * kWarps + 2 * b; };
     // the unit that takes a step
     auto owner = [&](int64_t step) {
         const int64_t head = rest * (base + 1);
@@ -657,11 +661,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             first = begins ? unit : owner(start);
             last = ends ? unit : owner(start + p.s.tiles - 1);
         }
-        const bool inside = first >= block0 && last < block0 + busy;
-        const bool in_ring = inside && g + (t_end - t_begin) == g1;  // nothing more comes into the ring
-        const int64_t slot = 2 * (int64_t)self + (begins ? 1 : 0);
-        float2* part_ml = in_ring ? sm.ml[warp] : parts.ml + slot * kRows;
-        float* part_o = in_ring ? reinterpret_cast<float*>(&ws) : parts.o + slot * kRows * D;
+        const bool in_ring = g + (t_end - t_begin) == g1;  // nothing more comes into the ring
+        float2* part_ml = in_ring ? sm.ml[warp] : parts.ml + (int64_t)self * kRows;
+        float* part_o = in_ring ? reinterpret_cast<float*>(&ws) : parts.o + (int64_t)self * kRows * D;
 #pragma unroll
         for (int u = 0; u < 2 * NB; ++u) {
 #pragma unroll
@@ -692,17 +694,20 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             }
         }
         if (lane == 0 && !(begins && ends)) {
-            if (inside ? begins : warp == 0 && first < block0 && last < block0 + busy) {
+            const int64_t block1 = block0 + busy;  // behind the block's units
+            if (begins || (warp == 0 && g == g0)) {
                 Job job;
                 job.first = first;
-                job.parts = (int)(last - first + 1);
+                job.parts = (int)(min(last, block1 - 1) - max(first, block0) + 1);
                 job.rows = nrows;
                 job.head = p.head;
                 job.row0 = e.c0 * a.group;
-                (inside ? sm.own[warp] : sm.early) = job;
+                job.begins = first >= block0;
+                job.ends = last < block1;
+                sm.job[begins ? warp : kWarps] = job;
             }
-            if (inside && !in_ring) sm.outside[warp] = 1;
-            if (last >= block0 + busy && g + (t_end - t_begin) == g1 && warp == busy - 1) sm.beyond = 1;
+            if (!in_ring) sm.outside[warp] = 1;
+            if (last >= block1 && warp == busy - 1) sm.beyond = 1;
         }
         g += t_end - t_begin;
         if (g < g1) {
@@ -718,30 +723,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     }
     __syncthreads();
 
-    // ---- joining
-    if (threadIdx.x == 0 && sm.beyond) set_flag(&parts.flag[blockIdx.x], parts.nonce);
-    const Job job = sm.early;
-    if (warp == 0 && job.parts) {
-        const uint64_t t0 = globaltimer();
-        bool all;
-        do {
-            all = true;
-            for (int i = (int)quot(job.first, busy) + lane; i < (int)blockIdx.x; i += 32)
-                all &= get_flag(&parts.flag[i]) == parts.nonce;
-            all = __all_sync(0xffffffffu, all);
-        } while (!all && __all_sync(0xffffffffu, globaltimer() - t0 < kWaitNs));
-        if (!all) sm.abort = 1;
-        for (int i = (int)quot(job.first, busy) + lane; i < (int)blockIdx.x; i += 32) parts.flag[i] = 0;
-    }
-    // items within the block: a warp a row
-    uint32_t jobs = __ballot_sync(0xffffffffu, lane < busy && sm.own[lane % kWarps].parts > 0);
+    // ---- joining: the block's parts, a warp a row
+    uint32_t jobs = __ballot_sync(0xffffffffu, lane <= kWarps && sm.job[min(lane, kWarps)].parts > 0);
+    bool across = false;
     for (int at = 0; jobs; jobs &= jobs - 1) {
-        const int w0 = __ffs(jobs) - 1;
-        const Job& own = sm.own[w0];
-        const int n = own.parts, tail = w0 + n - 1;
-        const bool outside = sm.outside[tail];  // the last part, in the workspace
-        const int64_t far = (int64_t)2 * (blockIdx.x * kWarps + tail) * kRows;
-        for (int r = (warp + kWarps - at) % kWarps; r < own.rows; r += kWarps) {
+        const int which = __ffs(jobs) - 1, w0 = which % kWarps;
+        const Job& job = sm.job[which];
+        const int n = job.parts, tail = w0 + n - 1;
+        // the last part may lie in the workspace (but not where its warp began the item)
+        const bool outside = sm.outside[tail] && (n > 1 || !job.begins);
+        const int64_t far = ((int64_t)blockIdx.x * kWarps + tail) * kRows;
+        const bool whole = job.begins && job.ends;
+        across |= !whole;
+        for (int r = (warp + kWarps - at) % kWarps; r < job.rows; r += kWarps) {
             const Sum<D> s = sum_parts<D>(
                 n, 0, 1, lane,
                 [&](int j) { return outside && j == n - 1 ? parts.ml[far + r] : sm.ml[w0 + j][r]; },
@@ -749,49 +743,69 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                     return outside && j == n - 1 ? parts.o + (far + r) * D
                                                  : reinterpret_cast<const float*>(&sm.w[w0 + j]) + r * D;
                 });
-            write_row<D, T>(a, own, r, s, lane);
-        }
-        at = (at + own.rows) % kWarps;
-    }
-    if (job.parts) {
-        __syncthreads();  // the rings are free, the flags were there
-        struct alignas(16) Row {  // acc is read 16 bytes at a time
-            float acc[D], m, L;
-        };
-        static_assert(sizeof(Row) * kWarps <= sizeof(sm.w), "the ring holds the warps' sums");
-        Row* rows = reinterpret_cast<Row*>(sm.w);
-        const int b0 = (int)quot(job.first, busy), w0 = (int)(job.first - (int64_t)b0 * busy);
-        const int per = max(1, kWarps / job.rows);  // warps that share a row
-        for (int r0 = 0; r0 < job.rows && !sm.abort; r0 += kWarps / per) {
-            const int r = r0 + warp / per, sub = warp % per;
-            const bool mine = warp / per < kWarps / per && r < job.rows;
-            auto at = [&](int i) {  // part i of the row
-                const int v = w0 + i, b = (int)((unsigned)v / (unsigned)busy);
-                const int64_t w = (int64_t)(b0 + b) * kWarps + v - b * busy;
-                return (2 * w + (i == 0 ? 1 : 0)) * kRows + r;
-            };
-            Sum<D> s;
-            if (mine)
-                s = sum_parts<D>(
-                    job.parts, sub, per, lane, [&](int i) { return __ldcg(&parts.ml[at(i)]); },
-                    [&](int i) -> const float* { return parts.o + at(i) * D; });
-            if (per > 1) {
-                if (mine) {
-                    if (lane == 0) {
-                        rows[warp].m = s.m;
-                        rows[warp].L = s.L;
-                    }
+            if (whole) {
+                write_row<D, T>(a, job, r, s, lane);
+            } else {
+                const int64_t to = (block_slot(blockIdx.x) + (job.begins ? 1 : 0)) * kRows + r;
+                if (lane == 0) parts.ml[to] = make_float2(s.m, s.L);
+                float* dst = parts.o + to * D + lane * (D / 32);
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) rows[warp].acc[lane * (D / 32) + k] = s.acc[k];
-                }
-                __syncthreads();
-                if (mine && sub == 0)
-                    s = sum_parts<D>(
-                        per, 0, 1, lane, [&](int i) { return make_float2(rows[warp + i].m, rows[warp + i].L); },
-                        [&](int i) -> const float* { return rows[warp + i].acc; });
-                __syncthreads();
+                for (int k = 0; k < D / 32; ++k) dst[k] = s.acc[k];
             }
-            if (mine && sub == 0) write_row<D, T>(a, job, r, s, lane);
+        }
+        at = (at + job.rows) % kWarps;
+    }
+    if (across) {  // (the same for all warps)
+        __syncthreads();
+        if (threadIdx.x == 0 && sm.beyond) set_flag(&parts.flag[blockIdx.x], parts.nonce);
+        const Job job = sm.job[kWarps];
+        if (job.parts && job.ends) {  // an item of earlier blocks ends here
+            const int b0 = (int)quot(job.first, busy), n = (int)blockIdx.x - b0 + 1;
+            if (warp == 0) {
+                const uint64_t t0 = globaltimer();
+                bool all;
+                do {
+                    all = true;
+                    for (int i = b0 + lane; i < (int)blockIdx.x; i += 32) all &= get_flag(&parts.flag[i]) == parts.nonce;
+                    all = __all_sync(0xffffffffu, all);
+                } while (!all && __all_sync(0xffffffffu, globaltimer() - t0 < kWaitNs));
+                if (!all) sm.abort = 1;
+                for (int i = b0 + lane; i < (int)blockIdx.x; i += 32) parts.flag[i] = 0;
+            }
+            __syncthreads();
+            struct alignas(16) Row {  // acc is read 16 bytes at a time
+                float acc[D], m, L;
+            };
+            static_assert(sizeof(Row) * kWarps <= sizeof(sm.w), "the rings hold the warps' sums");
+            Row* rows = reinterpret_cast<Row*>(sm.w);
+            const int per = max(1, kWarps / job.rows);  // warps that share a row
+            for (int r0 = 0; r0 < job.rows && !sm.abort; r0 += kWarps / per) {
+                const int r = r0 + warp / per, sub = warp % per;
+                const bool mine = warp / per < kWarps / per && r < job.rows;
+                auto at = [&](int i) { return (block_slot(b0 + i) + (i == 0 ? 1 : 0)) * kRows + r; };
+                Sum<D> s;
+                if (mine)
+                    s = sum_parts<D>(
+                        n, sub, per, lane, [&](int i) { return __ldcg(&parts.ml[at(i)]); },
+                        [&](int i) -> const float* { return parts.o + at(i) * D; });
+                if (per > 1) {
+                    if (mine) {
+                        if (lane == 0) {
+                            rows[warp].m = s.m;
+                            rows[warp].L = s.L;
+                        }
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) rows[warp].acc[lane * (D / 32) + k] = s.acc[k];
+                    }
+                    __syncthreads();
+                    if (mine && sub == 0)
+                        s = sum_parts<D>(
+                            per, 0, 1, lane, [&](int i) { return make_float2(rows[warp + i].m, rows[warp + i].L); },
+                            [&](int i) -> const float* { return rows[warp + i].acc; });
+                    __syncthreads();
+                }
+                if (mine && sub == 0) write_row<D, T>(a, job, r, s, lane);
+            }
         }
     }
     if (threadIdx.x == 0 && sm.abort) *parts.status = TQ_ERR_DEVICE_TIMEOUT * 1000 - 80;
@@ -827,9 +841,9 @@ Parts carve(void* ws, int64_t blocks, size_t* bytes) {
     p.flag = (uint64_t*)at;
     at += align256(blocks * 8);
     p.ml = (float2*)at;
-    at += align256(2 * units * kRows * sizeof(float2));
+    at += align256((units + 2 * blocks) * kRows * sizeof(float2));
     p.o = (float*)at;
-    at += align256(2 * units * kRows * D * 4);
+    at += align256((units + 2 * blocks) * kRows * D * 4);
     *bytes = (size_t)(at - (char*)ws);
     return p;
 }

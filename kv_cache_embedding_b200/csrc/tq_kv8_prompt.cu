@@ -29,7 +29,7 @@
 // Every wait is bounded (1 s); a warp that gives up sets the abort flag and the
 // call's status.
 //
-// Measured (4096 tokens x 32 heads of 128 over 16384 keys, causal): 1040 us, 925
+// Measured (4096 tokens x 32 heads of 128 over 16384 keys, causal): 1030 us, 934
 // TFLOP/s.  The softmax bounds it: 64 keys take a stage 2100 cycles against 600
 // of MMAs, by issue slots (some 5 instructions an element of S, shared with the
 // conversion's) and the latency of its chain.  Tried and slower: a quarter or half

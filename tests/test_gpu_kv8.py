@@ -462,6 +462,18 @@ def test_attention_long(tq_lib, cuda, fmt, counts):
     check_attention(c, q, counts, lens)
 
 
+@pytest.mark.parametrize("heads,group,lens,counts", [
+    (1, 8, [60000], [1]), (1, 3, [20000, 5000, 9], [1, 4, 1]), (2, 16, [40000], [1]),
+    (3, 1, [7000, 7001, 31, 2500, 64], [1, 1, 1, 1, 1]), (1, 1, [30000, 31000], [12, 1])])
+def test_attention_over_many_blocks(tq_lib, cuda, heads, group, lens, counts):
+    """Items over many blocks, two and more of them in a block, short ones between."""
+    c = fill(tq_lib, cuda, "i8", heads, 64, 64, lens)
+    q = torch.randn(sum(counts), heads * group, 64, generator=gen(2)).to(torch.bfloat16).to(cuda)
+    first = check_attention(c, q, counts, lens)
+    for _ in range(3):
+        assert torch.equal(first, check_attention(c, q, counts, lens))
+
+
 def test_attention_many_entries(tq_lib, cuda):
     """More entries than threads of a block, most of them without queries."""
     lens = [(i * 7) % 90 for i in range(700)]
