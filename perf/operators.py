@@ -489,7 +489,7 @@ def run(s):
     if op == "attention":
         if own:
             return s["cache"].attention(0, s["q"], s["cu"], s["maxq"], causal=case["causal"],
-                                        window=case["window"])
+                                        window=case["window"] if case["causal"] else 0)
         return _attention(s)
     if op == "append":
         if own:
