@@ -435,6 +435,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     auto settle = [&]() {
         if (pend_stage >= 0 && lane < 4) sm.scale[warp][pend_stage][lane] = pend;
         pend_stage = -1;
+        __syncwarp();  // all lanes read the scales next, also where no tile is left to produce
     };
     auto produce = [&]() {
         settle();
