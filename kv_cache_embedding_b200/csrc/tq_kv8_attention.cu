@@ -5,8 +5,12 @@
 // Numerics.  Codes are exact halves; a query row times a power of two is a row
 // of halves (row_unit), so <q, c> is a sum of exact products in fp32.  The
 // block scales never touch the codes: s_k multiplies the logit, s_v the
-// probability, which is rounded to a half relative to the running largest s_v
-// (one rounding of 2^-11; the running maximum, sum and output are fp32).
+// probability, and the product is rounded to a half (2^-11) in units of its own
+// row's: with m the row's largest logit so far and q that of l + log2 s_v, rounded
+// down, it is multiplied by 2^(m - q + 14), which puts the row's largest product
+// between 2^13 and 2^15; what is smaller than halves' normal range is off by 2^-38 of
+// that largest one.  Keys that the row does not see have no part in the unit.
+// Maximum, sum and output are fp32.
 //
 // Work.  Reading the cache is the cost (2 d bytes a token and KV head for up to
 // 16 rows), so every warp is a stream of its own: it takes an equal, contiguous
@@ -484,7 +488,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         // the query rows as MMA columns: this thread loads row 8 nb + r0, and keeps
         // the sums of rows 8 nb + 2 c2 + {0, 1}: column 2 nb + {0, 1}
         uint32_t qf[NB][CH][2];
-        float sl[2 * NB], m[2 * NB], L[2 * NB];
+        float sl[2 * NB], m[2 * NB], q2[2 * NB], L[2 * NB];  // q2: of l + log2 s_v
         int lim[2 * NB], low[2 * NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -513,10 +517,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                 sl[u] = a.scale_log2 / __shfl_sync(0xffffffffu, unit_q, 4 * (2 * c2 + j));
                 lim[u] = a.causal ? min(pos, e.len - 1) : e.len - 1;
                 low[u] = below_window(a, pos);
-                m[u] = -INFINITY;
+                m[u] = q2[u] = -INFINITY;
                 L[u] = 0.f;
             }
         }
+        // A column's sums o are in units of 2^-unit (a row of zero scales: any unit)
+        auto unit_of = [](float m, float q) { return (int)floorf(fminf(m - q, 106.f)) + 14; };
         // keys below `clear` and above `low_any` need no mask for any row
         const int clear = a.causal ? min(e.len - e.qn, e.len - 1) : e.len - 1;
         const int low_any = below_window(a, e.len - 1);
@@ -527,7 +533,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             for (int i = 0; i < CH; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[nb][i][k] = 0.f;
-        float R = 0.f;  // running largest value scale: o is in units of it
 
         for (int t = t_begin; t < t_end; ++t) {
             const int key0 = (p.s.tile0 + t) * kTile;
@@ -563,21 +568,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             }
             const bool masked = key0 + kTile - 1 > clear || key0 <= low_any || sc.x == -INFINITY ||
                                 sc.y == -INFINITY;
-            const float vmax = fmaxf(sc.z, sc.w);
-            const float shrink = vmax > R ? R / vmax : 1.f;
-            R = fmaxf(R, vmax);
-            // (scales below fp32's normal range have no reciprocal: their values count as 0)
-            const float inv = R >= 1.17549435e-38f ? 1.f / R : 0.f;
-            const float w[2] = {sc.z * inv, sc.w * inv};
+            const float vs[2] = {sc.z, sc.w}, es[2] = {scale_exp(sc.z), scale_exp(sc.w)};
             uint32_t pf[NB][2][2];
             float alpha[2 * NB];
             bool rescale = false;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                float mx[2] = {m[2 * nb], m[2 * nb + 1]};
+                float mx[2][2], w[2][2];  // [16 keys][column]
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const float ks = b == 0 ? sc.x : sc.y;
+                    mx[b][0] = mx[b][1] = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int u = 2 * nb + (k & 1);
@@ -587,33 +588,46 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                             if (key > lim[u] || key <= low[u] || ks == -INFINITY) l = -INFINITY;
                         }
                         s[nb][b][k] = l;
-                        mx[k & 1] = fmaxf(mx[k & 1], l);
+                        mx[b][k & 1] = fmaxf(mx[b][k & 1], l);
                     }
                 }
+                float base[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int u = 2 * nb + j;
+                    float top = fmaxf(mx[0][j], mx[1][j]), topq = fmaxf(mx[0][j] + es[0], mx[1][j] + es[1]);
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], x));
-                    const float base = mx[j] == -INFINITY ? 0.f : mx[j];
-                    alpha[u] = ex2(m[u] - base);
-                    m[u] = mx[j];
-                    mx[j] = base;
-                    L[u] *= alpha[u];
-                    alpha[u] *= shrink;
+                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    if (es[0] == es[1]) {  // (all tiles where a page holds them whole)
+                        topq = top + es[0];
+                    } else {
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) topq = fmaxf(topq, __shfl_xor_sync(0xffffffffu, topq, x));
+                    }
+                    const float m0 = m[u];
+                    const int unit0 = unit_of(m0, q2[u]);
+                    m[u] = fmaxf(m0, top);
+                    q2[u] = fmaxf(q2[u], topq);
+                    const int unit = unit_of(m[u], q2[u]);
+                    base[j] = m[u] == -INFINITY ? 0.f : m[u];
+                    L[u] *= ex2(m0 - base[j]);
+                    alpha[u] = ex2(m0 - base[j] + (float)(unit - unit0));
                     rescale |= alpha[u] != 1.f;
+                    // (a hidden page's may be anything: it meets zeros)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) w[b][j] = fminf(vs[b] * pow2(unit), kLargestFloat);
                 }
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     float pr[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        pr[k] = ex2(s[nb][b][k] - mx[k & 1]);
+                        pr[k] = ex2(s[nb][b][k] - base[k & 1]);
                         L[2 * nb + (k & 1)] += pr[k];
                     }
                     // keys x columns, transposed into the B operand
-                    pf[nb][b][0] = movm(pack_half2(pr[0] * w[b], pr[1] * w[b]));
-                    pf[nb][b][1] = movm(pack_half2(pr[2] * w[b], pr[3] * w[b]));
+                    pf[nb][b][0] = movm(pack_half2(pr[0] * w[b][0], pr[1] * w[b][1]));
+                    pf[nb][b][1] = movm(pack_half2(pr[2] * w[b][0], pr[3] * w[b][1]));
                 }
             }
             if (__any_sync(0xffffffffu, rescale)) {
@@ -671,16 +685,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             for (int x = 4; x < 32; x <<= 1) L[u] += __shfl_xor_sync(0xffffffffu, L[u], x);
             const int r = 8 * (u >> 1) + 2 * c2 + (u & 1), j = u & 1, nb = u >> 1;
             if (r >= nrows) continue;
+            const float size = pow2(-unit_of(m[u], q2[u]));
             if (begins && ends) {
                 const int64_t tok = e.c0 + r / a.group;
                 const int hq = p.head * a.group + r % a.group;
-                const float n = L[u] > 0.f ? R / L[u] : (L[u] == 0.f ? 0.f : L[u]);
+                const float n = L[u] > 0.f ? 1.f / L[u] : (L[u] == 0.f ? 0.f : L[u]);
                 T* out = (T*)a.out + (tok * a.heads_q + hq) * D + 2 * r0;
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
                     Pack<T, 2> v;
-                    from_f(o[nb][ch][j] * n, v.v[0]);
-                    from_f(o[nb][ch][2 + j] * n, v.v[1]);
+                    from_f(o[nb][ch][j] * size * n, v.v[0]);
+                    from_f(o[nb][ch][2 + j] * size * n, v.v[1]);
                     *reinterpret_cast<Pack<T, 2>*>(out + 16 * ch) = v;
                 }
                 if (a.lse && r0 == 0)
@@ -691,7 +706,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch)
                     *reinterpret_cast<float2*>(dst + 16 * ch) =
-                        make_float2(o[nb][ch][j] * R, o[nb][ch][2 + j] * R);
+                        make_float2(o[nb][ch][j] * size, o[nb][ch][2 + j] * size);
             }
         }
         if (lane == 0 && !(begins && ends)) {

@@ -85,6 +85,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The exponent e of a value scale, 2^e <= s < 2^(e + 1) (below fp32's normal range
+// -127, an upper bound still); -infinity for 0.  2^e for -126 <= e <= 127.
+__device__ __forceinline__ float scale_exp(float s) {
+    return s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : -INFINITY;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+constexpr float kLargestFloat = 3.40282347e38f;
+
 // The power of two that brings a row's largest magnitude into [1, 2): with it a
 // 16-bit row is a row of halves, exact down to 2^-14 of the largest and within
 // 2^-25 of it below.

@@ -1,12 +1,14 @@
 // Attention over the 8-bit paged cache, many query rows (prompts, chunks behind
 // a prefix, drafts): the sums of tq_kv8_attention.cu on the sm_100a tensor cores.
 //
-//   S = Q C_k^T   (rows x 128 keys),   P = 2^(S s_k s_q - m),   O += (P s_v / R) C_v
+//   S = Q C_k^T   (rows x 128 keys),   P = 2^(S s_k s_q - m),   O += (P s_v 2^(m - r)) C_v
 //
 // with the codes C as exact halves, Q a row of halves times a power of two, s_k
-// and s_v one number per 16 keys (a page at least), m the row's reference
-// maximum and R the largest s_v of the item's keys; P is rounded to a half once,
-// sums are fp32.
+// and s_v one number per 16 keys (a page at least).  m and r are the row's own: whole
+// numbers near the largest logit and the largest log2 (P s_v) + m of the keys that it
+// sees, so that P s_v 2^(m - r) is rounded to a half (2^-11) with the largest one at
+// 2^5 at least: what is smaller than halves' normal range is off by 2^-30 of that one,
+// and no page that the row does not see has a part in it.  Sums are fp32.
 //
 // A CTA runs items of 256 rows (two stages of 128) of one entry and KV head over
 // tiles of 128 keys; the steps (item x tile) of the whole batch are shared out
@@ -15,17 +17,17 @@
 // joined by k_prompt_merge.  Warps:
 //   0-3, 4-7  softmax of stage 0, 1: a thread a row, half a tile (64 keys) at a time.
 //             Loads its query row, turns S (tensor memory) into P in place, rescales
-//             O only when the row's maximum has grown by more than 2^8 (the reference
-//             m then follows; P <= 2^8 meanwhile, far inside a half's range), writes
-//             the result.
+//             O only when the row's largest product has grown by more than 2^8 (the
+//             reference r then follows; the product is below 2^15 meanwhile, inside a
+//             half's range), writes the result.
 //   8-11      codes -> halves: from the TMA ring (128 keys x d bytes) into the
 //             swizzled operand tiles of K (K-major) and V (the same rows, read
 //             MN-major), with the tile's scales.
 //   12, 15    issue the MMAs of stage 0, 1: per half O += P V, then S of the half
 //             two further, so the softmax finds its next S complete.
 //   13        the TMA loads, a page table lookup a box, a tile ahead.
-//   14        walks the CTA's share and hands the others its items, with R, through
-//             a short ring: lengths, divisions and lookups are off their path.
+//   14        walks the CTA's share and hands the others its items through a short
+//             ring: lengths, divisions and lookups are off their path.
 // Every wait is bounded (1 s); a warp that gives up sets the abort flag and the
 // call's status.
 //
@@ -55,7 +57,9 @@ constexpr int kGroups = kPT / 16;   // scale groups of a tile
 constexpr int kRing = 4;            // tiles whose scales are kept
 constexpr int kWorks = 4;           // items that are handed out ahead
 constexpr uint32_t kTmemCols = 512;
-constexpr float kGrow = 8.f;        // log2 of how far P may pass 1
+constexpr float kGrow = 8.f;        // log2 of how far a probability may pass 1
+constexpr float kRoom = 14.f;       // P stays below 2^(kRoom + 1), a half's range,
+constexpr float kStart = 6.f;       // and is put between 2^(kStart - 1) and 2^(kStart + 1)
 
 // A CTA's piece of an item, as the warps get it.
 struct Work {
@@ -64,7 +68,6 @@ struct Work {
     int row0, rows;   // first of the item's rows (token x group), their number; 0: no more work
     int t0, t, t_end, nt;  // first tile of the item; the CTA's tiles t .. t_end of its nt
     int parts;        // CTAs that hold the item, where it begins here and goes on
-    float R;          // largest value scale of the CTA's keys
     int64_t c0;       // the entry's first query token
 };
 
@@ -73,7 +76,7 @@ struct PSmem {
     uint8_t q[2][kPM * D * 2];    // stages' queries: 64-coordinate blocks of 128 rows x 128 B
     uint8_t kv[4][kPT * D * 2];   // K of even, odd tiles, V of even, odd tiles
     uint8_t raw[2][kPT * D];      // codes as they arrive: K, V
-    float kscale[kRing][kGroups], vscale[kRing][kGroups];  // s_k, s_v / R
+    float kscale[kRing][kGroups], vscale[kRing][kGroups], vexp[kRing][kGroups];  // s_k, s_v, its exponent
     uint32_t absent[kRing];       // 16-key groups without a page
     Work work[kWorks];
     uint64_t raw_full[2], raw_empty[2], kv_full[4], kv_empty[4];
@@ -307,7 +310,9 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             const int pos = w.pos0 + tq, len = w.len;
             const int lim = valid && a.causal ? min(pos, len - 1) : len - 1;
             const int low = valid ? below_window(a, pos) : -1;
-            float m = -INFINITY;
+            // the references, whole numbers once there is a key: L is in units of 2^m,
+            // O of 2^r, lift is 2^(m - r)
+            float m = -INFINITY, r = -INFINITY, lift = 1.f;
             float2 L2 = make_float2(0.f, 0.f);
             const uint32_t first = halves, last = halves + 2 * (t_end - t_begin);
             for (int key0 = (w.t0 + t_begin) * kPT; halves < last; key0 += kPH) {
@@ -320,12 +325,14 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 tc_fence_after();
                 uint32_t s[2][32];
                 tmem_ld32(s_col, s[0]);
-                float cg[4];
+                float cg[4], tg[4];  // of 16 keys: the factor of S, the largest logit
 #pragma unroll
-                for (int g = 0; g < 4; ++g) cg[g] = sl * sm.kscale[rg][4 * h + g];
+                for (int g = 0; g < 4; ++g) {
+                    cg[g] = sl * sm.kscale[rg][4 * h + g];
+                    tg[g] = -INFINITY;
+                }
                 const uint32_t absent = sm.absent[rg] >> 4 * h & 15u;
                 const bool masked = __any_sync(0xffffffffu, key0 + kPH - 1 > lim || key0 <= low || absent);
-                float top = -INFINITY;
                 // 32 keys are on their way while the 32 before them are looked at
                 if (masked) {
 #pragma unroll
@@ -339,7 +346,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         for (int i = 0; i < 32; ++i) {
                             const float x = see >> i & 1u ? __uint_as_float(s[c][i]) * cg[2 * c + i / 16] : -INFINITY;
                             s[c][i] = __float_as_uint(x);
-                            top = fmaxf(top, x);
+                            tg[2 * c + i / 16] = fmaxf(tg[2 * c + i / 16], x);
                         }
                     }
 #pragma unroll
@@ -349,20 +356,27 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     for (int c = 0; c < 2; ++c) {
                         tmem_wait_ld();
                         if (c < 1) tmem_ld32(s_col + 32, s[1]);
-                        const float x0 = max16(&s[c][0]) * cg[2 * c], x1 = max16(&s[c][16]) * cg[2 * c + 1];
-                        top = max3(top, x0, x1);
+                        tg[2 * c] = max16(&s[c][0]) * cg[2 * c];
+                        tg[2 * c + 1] = max16(&s[c][16]) * cg[2 * c + 1];
                     }
                 }
-                // the reference follows when the maximum has grown past it by kGrow
-                const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
+                const float* ve = &sm.vexp[rg][4 * h];
+                const float top = fmaxf(max3(tg[0], tg[1], tg[2]), tg[3]);
+                const float topr = fmaxf(max3(tg[0] + ve[0], tg[1] + ve[1], tg[2] + ve[2]), tg[3] + ve[3]);
+                // the references follow when what they are of has grown out of their range
                 float shrink = 1.f;
-                if (grow) {
-                    shrink = ex2(m - top);  // 0 from -infinity
-                    m = top;
-                    L2.x *= shrink;
-                    L2.y *= shrink;
+                if (top > m + kGrow || topr > r + kRoom) {
+                    const float m0 = m, r0 = r;
+                    m = fmaxf(m, ceilf(top));
+                    // (far below the probabilities: out of fp32's range)
+                    r = max3(r, ceilf(topr) - kStart, m - 120.f);
+                    lift = ex2(m - r);
+                    const float f = ex2(m0 - m);  // 0 from -infinity
+                    L2.x *= f;
+                    L2.y *= f;
+                    shrink = ex2(r0 - r);
                 }
-                if (halves > first && __any_sync(0xffffffffu, grow)) {
+                if (halves > first && __any_sync(0xffffffffu, shrink != 1.f)) {
                     // O holds all halves before this one when the last one's MMAs are done
                     if (!wait(&sm.o_done[st][(halves - 1) & 1], ((halves - 1) >> 1) & 1)) {
                         ok = false;
@@ -386,7 +400,8 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int g = 2 * c + k;
-                        const float vw = sm.vscale[rg][4 * h + g];
+                        // (a hidden page's may be anything: it meets zeros)
+                        const float vw = fminf(sm.vscale[rg][4 * h + g] * lift, kLargestFloat);
                         const float2 cc = make_float2(cg[g], cg[g]), bb = make_float2(base, base);
                         const float2 ww = make_float2(vw, vw);
 #pragma unroll
@@ -415,9 +430,9 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             tc_fence_after();
             const float L = L2.x + L2.y;
             const bool begins = t_begin == 0, ends = t_end == w.nt;
-            const float R = w.R;
+            const float size = 1.f / lift;
             if (begins && ends) {
-                const float f = L > 0.f ? R / L : (L == 0.f ? 0.f : L);
+                const float f = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
                 T* out = (T*)a.out + (tok * a.heads_q + hq) * D;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -429,7 +444,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         for (int h = 0; h < 4; ++h) {
                             Pack<T, 8> y;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) from_f(__uint_as_float(o[8 * h + k]) * f, y.v[k]);
+                            for (int k = 0; k < 8; ++k) from_f(__uint_as_float(o[8 * h + k]) * size * f, y.v[k]);
                             *reinterpret_cast<Pack<T, 8>*>(out + c + 8 * h) = y;
                         }
                     }
@@ -449,8 +464,8 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
                             *reinterpret_cast<float4*>(parts.o + pr * D + c + k) =
-                                make_float4(__uint_as_float(o[k]) * R, __uint_as_float(o[k + 1]) * R,
-                                            __uint_as_float(o[k + 2]) * R, __uint_as_float(o[k + 3]) * R);
+                                make_float4(__uint_as_float(o[k]) * size, __uint_as_float(o[k + 1]) * size,
+                                            __uint_as_float(o[k + 2]) * size, __uint_as_float(o[k + 3]) * size);
                     }
                 }
                 if (begins && st == 0 && row == 0) {
@@ -476,8 +491,6 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                 const Work& w = sm.work[n % kWorks];
                 if (w.rows == 0) break;
                 const int t_end = w.t_end, len = w.len, slot = w.slot, head = w.head, tile0 = w.t0;
-                // (scales below fp32's normal range have no reciprocal: their values count as 0)
-                const float inv = w.R >= 1.17549435e-38f ? 1.f / w.R : 0.f;
                 // thread g < 8: s_k of the next tile's 16-key group g; 8..15: s_v; NaN: no page
                 auto load_scale = [&](int t) {
                     float x = 0.f;
@@ -508,7 +521,10 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                             const int rg = tile & (kRing - 1);
                             const uint32_t gone = __ballot_sync(0xffffffffu, tid < 8 && sc < 0.f);
                             if (tid < 8) sm.kscale[rg][tid] = fmaxf(sc, 0.f);
-                            else if (tid < 16) sm.vscale[rg][tid - 8] = sc * inv;
+                            else if (tid < 16) {
+                                sm.vscale[rg][tid - 8] = sc;
+                                sm.vexp[rg][tid - 8] = scale_exp(sc);
+                            }
                             if (tid == 0) sm.absent[rg] = gone;
                         }
                         const uint8_t* src = sm.raw[b];
@@ -715,13 +731,6 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         const int64_t last = g + w.nt - 1, head1 = rest * (base + 1);  // the item's last step: its CTA
                         w.parts = (int)(last < head1 ? quot(last, base + 1) : rest + quot(last - head1, base)) - unit + 1;
                     }
-                    const int p1 = (min(e.len, (w.t0 + w.t_end) * kPT) - 1) >> a.v.page_log2;
-#pragma unroll 4
-                    for (int p = (((w.t0 + t) * kPT) >> a.v.page_log2) + lane; p <= p1; p += 32) {
-                        const int pid = page_of(a.v, e.slot, p);
-                        if (pid >= 0) w.R = fmaxf(w.R, a.vs[(int64_t)pid * a.v.heads + head]);
-                    }
-                    w.R = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(w.R)));
                 }
                 ok = n < kWorks || wait(&sm.work_empty[n % kWorks], (n / kWorks - 1) & 1);
                 if (!ok) break;
