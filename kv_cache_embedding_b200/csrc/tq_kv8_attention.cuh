@@ -93,13 +93,14 @@ __device__ __forceinline__ float scale_exp(float s) {
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 constexpr float kLargestFloat = 3.40282347e38f;
 
-// The power of two that brings a row's largest magnitude into [1, 2): with it a
-// 16-bit row is a row of halves, exact down to 2^-14 of the largest and within
-// 2^-25 of it below.
+// The power of two that brings a row's largest magnitude into [2^15, 2^16), the top
+// of a half's range: with it a row of bf16 is a row of halves, exact down to 2^-32 of
+// the largest and within 2^-40 of it below; a row of f16 is never divided, so exact.
+// (A row below 2^-111 comes to less: 2^126 is the largest unit.)
 __device__ __forceinline__ float row_unit(float top) {
     int e = (int)(__float_as_uint(top) >> 23);
-    e = min(max(e, 1), 253);
-    return __uint_as_float((uint32_t)(254 - e) << 23);
+    e = min(max(e, 16), 254);
+    return __uint_as_float((uint32_t)(269 - e) << 23);
 }
 
 constexpr uint64_t kWaitNs = 1000000000ull;

@@ -136,3 +136,16 @@ def test_a_later_infinity(tq_lib, cuda):
         c.append(0, k, v, cu_of([100], cuda), 100)
         got.append(c.attention(0, q, cu_of([100], cuda), 100)[:96])
     assert torch.equal(*got)
+
+
+@pytest.mark.parametrize("count", [1, 40])
+def test_small_query_coordinates(tq_lib, cuda, count):
+    """A query's small coordinates count beside large ones: the large ones' keys are
+    0, so the logits are the small ones' alone."""
+    n = 200
+    c = fill(tq_lib, cuda, "i8", 1, 128, 64, [n])
+    c.k[..., :64] = 0
+    q = torch.randn(count, 2, 128, generator=gen(6))
+    q[..., 64:] *= 2.0 ** -20
+    q[..., :64] = 1.0
+    check(c, "i8", q.to(torch.bfloat16).to(cuda), [count], [n], scale=2.0 ** 20)
