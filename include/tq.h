@@ -413,7 +413,15 @@ TQ_API int tq_rope(const tq_rope_params_t *r, int64_t T, int heads, const void *
  * any bytes (none of the calls below reads them into a result).
  * Limits: d 64 or 128; page 16, 32, 64 or 128; heads, layers, slots,
  * max_pages, pages >= 1; pages * heads * page < 2^31; d_k and d_v 16-byte
- * aligned. */
+ * aligned.
+ * d_status: a step is a chain of calls that build on one another without the host
+ * looking between them.  The first refusal or time-out that a call of the cache
+ * finds on the device is left here, and as long as the word is not 0 the calls
+ * behind it stay clear of the cache: the page operations and tq_kv8_append change
+ * nothing, tq_kv8_read and tq_kv8_attention give what they give for slots of length
+ * 0.  tq_device_status reads it (once the calls are through); the caller sets it to
+ * 0, before the first call too.  NULL: no such word, and a caller has to look at a
+ * page operation's own status before it goes on. */
 typedef struct tq_kv8 {
     int32_t d, heads, page, format;
     int32_t layers, slots, max_pages, pages;
@@ -422,6 +430,7 @@ typedef struct tq_kv8 {
     int32_t *d_table;              /* [slots][max_pages] page ids; -1: none */
     int32_t *d_len;                /* [slots]                               */
     int32_t *d_refs;               /* [pages]                               */
+    int32_t *d_status;             /* [1], or NULL                          */
 } tq_kv8_t;
 
 /* operation ids for tq_kv8_workspace_bytes */
@@ -441,8 +450,8 @@ TQ_API size_t tq_kv8_workspace_bytes(int op, const tq_kv8_t *c, int n, int64_t t
  * holds pages or onto a parent of the same list; TQ_ERR_PAGES when too few
  * pages are free.  n = 0 is a no-op.  n <= 4096, else TQ_ERR_UNSUPPORTED.
  * d_ws: >= tq_kv8_workspace_bytes(TQ_KV8_OP_PAGES, c, n, 0, 0, 0).
- * The tables are taken as these calls leave them; entries out of range are
- * skipped. */
+ * A call that finds c->d_status set gives that status.  The tables are taken as
+ * these calls leave them; entries out of range are skipped. */
 
 /* Makes room for d_counts[i] more tokens in slot d_slots[i] and adds them to
  * its length (the tokens are then written by tq_kv8_append, layer by layer).

@@ -92,6 +92,7 @@ class tq_kv8_t(C.Structure):
         ("d_table", C.c_void_p),
         ("d_len", C.c_void_p),
         ("d_refs", C.c_void_p),
+        ("d_status", C.c_void_p),
     ]
 
 

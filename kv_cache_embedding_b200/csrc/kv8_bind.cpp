@@ -9,6 +9,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -41,7 +42,7 @@ struct Cache {
     c10::Device device;
     // per stream: calls of one stream follow one another
     std::unordered_map<cudaStream_t, at::Tensor> ws;
-    at::Tensor last;  // the workspace of the last call that leaves a status
+    at::Tensor status;  // c.d_status
 };
 
 const at::Tensor& tensor(PyObject* o, const char* name) {
@@ -104,6 +105,7 @@ const tq_rope_params_t* rope_params(PyObject* o) {
 struct Ws {
     void* ptr;
     size_t bytes;
+    at::Tensor owner;  // until the call is launched
 };
 Ws workspace(Cache* c, int op, int n, int64_t total, int max_q, int heads_q, cudaStream_t stream) {
     const size_t need = tq_kv8_workspace_bytes(op, &c->c, n, total, max_q, heads_q);
@@ -112,15 +114,16 @@ Ws workspace(Cache* c, int op, int n, int64_t total, int max_q, int heads_q, cud
         return at::detail::empty_cuda({(int64_t)(need < 256 ? 256 : need)}, at::kByte, c->device,
                                       std::nullopt);
     };
+    // in a capture the graph's own memory: graphs that run side by side share nothing
+    at::Tensor t;
     if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
-        // the graph's own memory: graphs that run side by side share nothing
-        c->last = fresh();
+        t = fresh();
     } else {
-        at::Tensor& t = c->ws[stream];
-        if (!t.defined() || (size_t)t.numel() < need) t = fresh();
-        c->last = t;
+        at::Tensor& kept = c->ws[stream];
+        if (!kept.defined() || (size_t)kept.numel() < need) kept = fresh();
+        t = kept;
     }
-    return {c->last.data_ptr(), (size_t)c->last.numel()};
+    return {t.data_ptr(), (size_t)t.numel(), t};
 }
 
 void expect_args(Py_ssize_t got, Py_ssize_t want) {
@@ -150,16 +153,16 @@ Batch batch(Cache* c, PyObject* slots, PyObject* cu) {
     }                            \
     END_HANDLE_TH_ERRORS
 
-// (address of a tq_kv8_t, a tensor of the cache) -> handle; the struct is copied.
+// (address of a tq_kv8_t, its status word) -> handle; the struct is copied.
 PyObject* py_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TQ_PY_BEGIN
     expect_args(n, 2);
-    const at::Tensor& k = tensor(a[1], "k");
+    const at::Tensor& status = tensor(a[1], "status");
     const auto* s = (const tq_kv8_t*)PyLong_AsVoidPtr(a[0]);
     if (PyErr_Occurred()) throw Fail();
     if (tq_kv8_workspace_bytes(TQ_KV8_OP_PAGES, s, 0, 0, 0, 0) == (size_t)-1)
         check("tq_kv8_workspace_bytes", TQ_ERR_UNSUPPORTED);
-    return PyCapsule_New(new Cache{*s, k.device(), {}, {}}, "tq.kv8", [](PyObject* o) {
+    return PyCapsule_New(new Cache{*s, status.device(), {}, status}, "tq.kv8", [](PyObject* o) {
         delete (Cache*)PyCapsule_GetPointer(o, "tq.kv8");
     });
     TQ_PY_END
@@ -244,15 +247,19 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TQ_PY_END
 }
 
-// (cache): waits for the stream
+// (cache): waits for the stream; what it raises it takes off the cache
 PyObject* py_status(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TQ_PY_BEGIN
     expect_args(n, 1);
     Cache* c = cache(a[0]);
-    if (!c->last.defined()) Py_RETURN_NONE;
     const c10::cuda::CUDAGuard guard(c->device);
     const cudaStream_t s = c10::cuda::getCurrentCUDAStream(c->device.index()).stream();
-    check("tq_device_status", tq_device_status(c->last.data_ptr(), s));
+    const int status = tq_device_status(c->c.d_status, s);
+    if (status != TQ_OK && status != TQ_ERR_CUDA) {
+        const c10::InferenceMode mode;  // (the cache may have been made in one)
+        c->status.zero_();
+    }
+    check("tq_device_status", status);
     Py_RETURN_NONE;
     TQ_PY_END
 }
@@ -351,7 +358,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const cudaStream_t s = c10::cuda::getCurrentCUDAStream(c->device.index()).stream();
     const int layer = int32(a[1], "layer"), causal = PyObject_IsTrue(a[7]), window = int32(a[8], "window");
     // (a call of bad sizes gets no workspace: the entry point names what is wrong)
-    Ws w = {nullptr, 0};
+    Ws w = {nullptr, 0, {}};
     if (max_q >= 0 && heads_q >= 1 && heads_q % c->c.heads == 0)
         w = workspace(c, TQ_KV8_OP_ATTENTION, b.ns, total, max_q, (int)heads_q, s);
     check("tq_kv8_attention",

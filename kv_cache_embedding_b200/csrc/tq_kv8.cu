@@ -61,6 +61,15 @@ struct AppendArgs {
 
 constexpr float kLargest = 1.7014118e38f;  // 2^127
 
+// The cache's status on its way into shared memory (a register would be spilled).
+__device__ __forceinline__ void pending_to(int32_t* s, const View& v) {
+    if (v.status)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                     ::"r"((uint32_t)__cvta_generic_to_shared(s)), "l"(v.status) : "memory");
+    else
+        *s = 0;
+}
+
 // The larger one of a and |b|, NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -77,6 +86,7 @@ template <typename T, int FMT, int VEC, int NI, int ROPE>
 __global__ __launch_bounds__(VEC == 8 ? 1024 : 256) void k_append(
     const AppendArgs a, const __grid_constant__ tq_rope_params_t rope) {
     __shared__ uint32_t s_red[2][32];
+    __shared__ int32_t s_held;
     grid_begin();
     const View& v = a.v;
     const int seq = blockIdx.x / a.ppb, pj = blockIdx.x - seq * a.ppb;
@@ -150,6 +160,7 @@ __global__ __launch_bounds__(VEC == 8 ? 1024 : 256) void k_append(
         }
         src[i] = x + row * a.x_ts + o1[i];
     }
+    if (threadIdx.x == 0) pending_to(&s_held, v);
     fetch();
     if (VEC == 8 && ROPE && turn) {
 #pragma unroll
@@ -204,9 +215,12 @@ __global__ __launch_bounds__(VEC == 8 ? 1024 : 256) void k_append(
         uint32_t* red = s_red[h & 1];
         const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = most;
+        if (h == h0 && threadIdx.x == 0) asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
+        const int held = h == h0 ? s_held : 0;
         const uint32_t lane = threadIdx.x & 31;
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < blockDim.x / 32 ? red[lane] : 0u));
+        if (held) return;  // (before the first store)
         const float s = fmaxf(s_old, __fdiv_rn(top, code_max<FMT>()));
         if (threadIdx.x == 0) a.scale[kv][ph] = s;
         // (below fp32's normal range a reciprocal may overflow: all times 2^64)
@@ -324,7 +338,9 @@ __global__ __launch_bounds__(kReadThreads) void k_read(View v, const int32_t* sl
     const int slot = slot_of(v, slots, seq);
     const int64_t c0 = max(cu[seq], 0), c1 = min((int64_t)cu[seq + 1], total);
     const int64_t b = (int64_t)begin[seq] + (int64_t)blk * tokens;
-    const int len = slot >= 0 ? length_of(v, slot) : 0;
+    const int held = v.status ? *v.status : 0;  // (through L1: nothing here has to agree on it)
+    int len = slot >= 0 ? length_of(v, slot) : 0;
+    if (held) len = 0;
     const int nt = (int)min((int64_t)tokens, c1 - c0 - (int64_t)blk * tokens);
     if (nt <= 0) return;
     const int chunks = v.d / 16, per = v.heads * chunks, n = nt * per;

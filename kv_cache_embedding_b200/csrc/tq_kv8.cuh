@@ -14,6 +14,7 @@ struct View {
     int d, heads, page, page_log2, slots, max_pages, pages;
     const int32_t* table;
     const int32_t* len;
+    int32_t* status;  // may be null
 };
 
 // tq_kv8_t's limits; null pointers where `pointers` is set.
@@ -32,6 +33,7 @@ inline View view(const tq_kv8_t* c) {
     v.pages = c->pages;
     v.table = c->d_table;
     v.len = c->d_len;
+    v.status = c->d_status;
     return v;
 }
 
@@ -40,6 +42,16 @@ inline int64_t layer_bytes(const tq_kv8_t* c) {
     return (int64_t)c->pages * c->heads * c->page * c->d;
 }
 inline int64_t layer_scales(const tq_kv8_t* c) { return (int64_t)c->pages * c->heads; }
+
+// The cache's status: 0 where nothing has gone wrong.  A block looks at it once (one
+// barrier, or one thread): a call on another stream may set it meanwhile.
+__device__ __forceinline__ int pending(const View& v) {
+    return v.status ? *(const volatile int32_t*)v.status : 0;
+}
+// The first one stands.
+__device__ __forceinline__ void leave_status(const View& v, int status) {
+    if (v.status) atomicCAS(v.status, 0, status);
+}
 
 // Slot of batch entry i, or -1; its length, limited to what its table can name.
 __device__ __forceinline__ int slot_of(const View& v, const int32_t* slots, int i) {

@@ -300,8 +300,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         prefetch_tmap(&vmap);
     }
     grid_begin();
+    const int held = pending(a.v);
     // (blocks are dispatched in order, and one that gives up has waited for a second)
-    if (blockIdx.x == 0 && threadIdx.x == 0) *parts.status = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *parts.status = held;
 
     // ---- the batch's steps and items: a run of entries a thread, prefixes over the block
     const int run = (a.ns + kThreads - 1) / kThreads;
@@ -329,7 +330,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             sm.warp_items[warp] = items;
             sm.warp_most[warp] = most;
         }
-        __syncthreads();
+        if (__syncthreads_or(held)) {
+            empty_rows<D, T>(a);
+            return;
+        }
         for (int w = 0; w < warp; ++w) {
             steps += sm.warp_steps[w];
             items += sm.warp_items[w];
@@ -824,7 +828,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             }
         }
     }
-    if (threadIdx.x == 0 && sm.abort) *parts.status = TQ_ERR_DEVICE_TIMEOUT * 1000 - 80;
+    if (threadIdx.x == 0 && sm.abort) {
+        *parts.status = TQ_ERR_DEVICE_TIMEOUT * 1000 - 80;
+        leave_status(a.v, TQ_ERR_DEVICE_TIMEOUT * 1000 - 80);
+    }
 }
 
 constexpr int kMaxBlocks = 148;  // the workspace's size

@@ -64,6 +64,19 @@ __device__ __forceinline__ Entry entry_of(const Attn& a, int i) {
     e.len = e.slot >= 0 ? length_of(a.v, e.slot) : 0;
     return e;
 }
+// A call that finds the cache's status set: no row sees a key.  (All of the grid's
+// threads; a block that saw the word before it was set may write rows too.)
+template <int D, typename T>
+__device__ __forceinline__ void empty_rows(const Attn& a) {
+    const int64_t t0 = max(a.cu[0], 0), rows = (min((int64_t)a.cu[a.ns], a.total_q) - t0) * a.heads_q;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t at = block * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * gridDim.y * blockDim.x;
+    uint4* out = reinterpret_cast<uint4*>((T*)a.out + t0 * a.heads_q * D);
+    for (int64_t i = at; i < rows * (D / 8); i += step) out[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+        for (int64_t i = at; i < rows; i += step) a.lse[t0 * a.heads_q + i] = -INFINITY;
+}
+
 // First key that any query of the entry sees.
 __device__ __forceinline__ int first_key(const Attn& a, const Entry& e) {
     return a.window > 0 ? (int)max((int64_t)0, (int64_t)e.len - e.qn - a.window + 1) : 0;

@@ -80,6 +80,12 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* tmp, int64_t* 
     return r;
 }
 
+// Thread 0 gives a plan up: the status that held already, or a new one.
+__device__ __forceinline__ void refuse(const View& v, const PagesWs& w, int held, int status) {
+    w.head[0] = held ? held : status;
+    if (!held) leave_status(v, status);
+}
+
 __device__ __forceinline__ int pages_for(const View& v, int64_t tokens) {
     return (int)((tokens + v.page - 1) >> v.page_log2);
 }
@@ -125,7 +131,8 @@ __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t
     __shared__ int32_t s_base[kMaxList];  // first of the entry's new pages
     grid_begin();
     const int per = (n + kPT - 1) / kPT;  // entries of a thread
-    bool bad = repeated(v, slots, nullptr, n, w.marks);
+    const int held_status = threadIdx.x == 0 ? pending(v) : 0;
+    bool bad = repeated(v, slots, nullptr, n, w.marks) || held_status;
     if (threadIdx.x == 0) w.head[1] = 0;
     int at[kPer], more[kPer], need[kPer];
     bool shared_page = false;
@@ -176,7 +183,7 @@ __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t
     // the lowest `total` free pages
     int64_t found = 0;
     if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) w.head[0] = TQ_ERR_ARG;
+        if (threadIdx.x == 0) refuse(v, w, held_status, TQ_ERR_ARG);
         return;
     }
     for (int64_t p0 = 0; p0 < v.pages && found < total; p0 += 4 * kPT) {
@@ -198,7 +205,7 @@ __global__ __launch_bounds__(kPT) void k_reserve(View v, int32_t* table, int32_t
         found += got;
     }
     if (found < total) {
-        if (threadIdx.x == 0) w.head[0] = TQ_ERR_PAGES;
+        if (threadIdx.x == 0) refuse(v, w, 0, TQ_ERR_PAGES);
         return;
     }
     __syncthreads();
@@ -248,14 +255,15 @@ __global__ __launch_bounds__(kPT) void k_fork(View v, int32_t* table, int32_t* l
                                               int n, const int32_t* parents,
                                               const int32_t* children, PagesWs w) {
     grid_begin();
-    bool bad = repeated(v, children, parents, n, w.marks);
+    const int held = threadIdx.x == 0 ? pending(v) : 0;
+    bool bad = repeated(v, children, parents, n, w.marks) || held;
     for (int i = threadIdx.x; i < n; i += kPT) {
         const int p = parents[i], c = children[i];
         if ((unsigned)p >= (unsigned)v.slots || (unsigned)c >= (unsigned)v.slots) bad = true;
         else bad |= len[c] != 0;
     }
     if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) w.head[0] = TQ_ERR_ARG;
+        if (threadIdx.x == 0) refuse(v, w, held, TQ_ERR_ARG);
         return;
     }
     for (int i = threadIdx.x >> 5; i < n; i += kPT / 32) {
@@ -275,11 +283,12 @@ __global__ __launch_bounds__(kPT) void k_truncate(View v, int32_t* table, int32_
                                                   const int32_t* slots,
                                                   const int32_t* lens, PagesWs w) {
     grid_begin();
-    bool bad = repeated(v, slots, nullptr, n, w.marks);
+    const int held = threadIdx.x == 0 ? pending(v) : 0;
+    bool bad = repeated(v, slots, nullptr, n, w.marks) || held;
     for (int i = threadIdx.x; i < n; i += kPT)
         bad |= (unsigned)slots[i] >= (unsigned)v.slots || lens[i] < 0;
     if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) w.head[0] = TQ_ERR_ARG;
+        if (threadIdx.x == 0) refuse(v, w, held, TQ_ERR_ARG);
         return;
     }
     for (int i = threadIdx.x >> 5; i < n; i += kPT / 32) {
@@ -302,8 +311,13 @@ __global__ __launch_bounds__(kPT) void k_compact(View v, int32_t* refs, PagesWs 
     grid_begin();
     const int64_t run = ((int64_t)v.pages + kPT - 1) / kPT;
     const int64_t p0 = min((int64_t)v.pages, threadIdx.x * run), p1 = min((int64_t)v.pages, p0 + run);
+    const int held = threadIdx.x == 0 ? pending(v) : 0;
     int64_t live = 0, L, moves;
     for (int64_t p = p0; p < p1; ++p) live += refs[p] > 0;
+    if (__syncthreads_or(held)) {
+        if (threadIdx.x == 0) w.head[0] = held;
+        return;
+    }
     block_scan(live, tmp, &L);
     int64_t movers = 0, holes = 0;
     for (int64_t p = p0; p < p1; ++p) {

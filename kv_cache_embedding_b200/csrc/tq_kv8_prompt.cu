@@ -203,7 +203,10 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
         }
         int64_t* sums = pre + kPThreads + 40;
         if (lane == 31) sums[warp] = inc;
-        __syncthreads();
+        if (__syncthreads_or(threadIdx.x == 0 && pending(a.v))) {  // (k_prompt_merge writes the rows)
+            if (threadIdx.x == 0) parts.block_status[unit] = 0;
+            return;
+        }
         for (int w = 0; w < warp; ++w) inc += sums[w];
         pre[threadIdx.x + 1] = inc;
         if (threadIdx.x == 0) pre[0] = 0;
@@ -762,20 +765,25 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
 }
 
 // Joins the parts of the items that were cut: blocks (u, y) the item that begins
-// in CTA u, a warp a row, 4 coordinates a lane (d = 128) or 2.
+// in CTA u, a warp a row, 4 coordinates a lane (d = 128) or 2.  With the cache's status
+// set it writes the rows of a call that saw no key.
 template <int D, typename T>
 __global__ __launch_bounds__(256) void k_prompt_merge(const Attn a, const PromptParts parts, int blocks) {
     const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_begin();
+    const int held = pending(a.v);
     if (u == 0 && blockIdx.y == 0) {
         int st = 0;
         for (int i = threadIdx.x; i < blocks; i += 256) st |= parts.block_status[i] != 0;
         st = __syncthreads_or(st);
+        const int status = st ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 81 : held;
         // (the few-rows kernel of the call has set the word; a time-out stands)
-        if (threadIdx.x == 0 && (st || !parts.keep_status)) *parts.status = st ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 81 : 0;
+        if (threadIdx.x == 0 && (st || !parts.keep_status)) *parts.status = status;
+        if (threadIdx.x == 0 && st) leave_status(a.v, status);
     }
     const Cut c = parts.cut[u];
-    if (c.parts == 0) return;
+    if (held) empty_rows<D, T>(a);
+    if (held || c.parts == 0) return;
     constexpr int E = D / 32;
     auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)u + 1 : 2 * (int64_t)(u + i); };
     for (int r = blockIdx.y * 8 + warp; r < c.rows; r += gridDim.y * 8) {

@@ -70,8 +70,11 @@ class KV8Cache:
 
     KV8Cache.empty(...) allocates them.  A step of an engine: reserve (room for
     the new tokens, lengths move on), then layer by layer append and attention.
-    Page calls check on the device; status() waits and raises what the last one
-    found."""
+    The calls check on the device.  From the first one that is refused there (or
+    times out) until status() has raised it, further calls leave the cache as it
+    is: the step's append writes nothing, its attention gives zeros.  Where a
+    reserve was refused the step can simply be repeated; lengths are as they were
+    before it."""
 
     def __init__(self, k, v, kscale, vscale, table, lens, refs):
         if k.dim() != 5 or k.dtype not in _FORMATS:
@@ -91,11 +94,13 @@ class KV8Cache:
         self.table, self.lens, self.refs = table, lens, refs
         self.layers, self.pages, self.heads, self.page, self.d = layers, pages, heads, page, d
         self.slots, self.device = lens.shape[0], k.device
+        self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self.c = B.tq_kv8_t(d, heads, page, _FORMATS[k.dtype], layers, self.slots, table.shape[1],
                             pages, k.data_ptr(), v.data_ptr(), kscale.data_ptr(),
-                            vscale.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr())
+                            vscale.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
+                            self._status.data_ptr())
         # the workspaces live there, one a stream
-        self._h = N.cache(ctypes.addressof(self.c), k)
+        self._h = N.cache(ctypes.addressof(self.c), self._status)
 
     @classmethod
     def empty(cls, layers, pages, heads, d, slots, max_pages, page=64, dtype=torch.int8,
@@ -133,8 +138,8 @@ class KV8Cache:
         N.compact(self._h)
 
     def status(self):
-        """Waits for the stream and raises what the last page or attention call
-        found on the device."""
+        """Waits for the stream and raises the first refusal or time-out since the
+        last status(); the cache can be used again."""
         N.status(self._h)
 
     # ---- tokens
