@@ -10,6 +10,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/InferenceMode.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -247,17 +248,31 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TQ_PY_END
 }
 
-// (cache): waits for the stream; what it raises it takes off the cache
+// Other threads of the interpreter go on meanwhile.
+struct NoGil {
+    PyThreadState* state = PyEval_SaveThread();
+    ~NoGil() { PyEval_RestoreThread(state); }
+};
+
+// (cache): waits for the device -- a call may have run on any stream, in a graph
+// too; what it raises it takes off the cache
 PyObject* py_status(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TQ_PY_BEGIN
     expect_args(n, 1);
     Cache* c = cache(a[0]);
     const c10::cuda::CUDAGuard guard(c->device);
-    const cudaStream_t s = c10::cuda::getCurrentCUDAStream(c->device.index()).stream();
-    const int status = tq_device_status(c->c.d_status, s);
+    TORCH_CHECK(c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None,
+                "status() waits for the device, which a graph capture cannot");
+    const c10::cuda::CUDAStream s = c10::cuda::getCurrentCUDAStream(c->device.index());
+    {
+        const NoGil no_gil;
+        c10::cuda::device_synchronize();
+    }
+    const int status = tq_device_status(c->c.d_status, s.stream());
     if (status != TQ_OK && status != TQ_ERR_CUDA) {
         const c10::InferenceMode mode;  // (the cache may have been made in one)
         c->status.zero_();
+        s.synchronize();  // (the next call may be on another stream)
     }
     check("tq_device_status", status);
     Py_RETURN_NONE;

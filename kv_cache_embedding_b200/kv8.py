@@ -138,8 +138,9 @@ class KV8Cache:
         N.compact(self._h)
 
     def status(self):
-        """Waits for the stream and raises the first refusal or time-out since the
-        last status(); the cache can be used again."""
+        """Waits for the device (calls on every stream and replayed graphs) and raises
+        the first refusal or time-out since the last status(); after that the cache
+        can be used again.  Not during a capture."""
         N.status(self._h)
 
     # ---- tokens

@@ -125,3 +125,58 @@ def test_a_cache_made_in_inference_mode(tq_lib, cuda):
     c.reserve(ints([0], cuda), ints([40], cuda))
     refused(tq_lib, c, "PAGES")
     c.status()
+
+
+def test_status_after_another_stream(tq_lib, cuda):
+    """status() sees what a call on any stream found, also one that has not begun."""
+    c = make_cache(tq_lib, cuda, page=16, slots=2, max_pages=4, pages=2)
+    slots, many, one = ints([0], cuda), ints([40], cuda), ints([1], cuda)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    c.reserve(slots, one)
+    c.status()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+        c.reserve(slots, many)
+    refused(tq_lib, c, "PAGES")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        torch.cuda._sleep(200_000_000)
+        c.reserve(slots, many)
+    with torch.cuda.stream(side):
+        g.replay()
+    refused(tq_lib, c, "PAGES")
+
+
+def test_status_while_capturing(tq_lib, cuda):
+    """A capture cannot wait: status() says so and leaves the capture as it was."""
+    c = make_cache(tq_lib, cuda, page=16, slots=2, max_pages=4, pages=2)
+    slots, one = ints([0], cuda), ints([1], cuda)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.reserve(slots, one)
+        with pytest.raises(RuntimeError):
+            c.status()
+    g.replay()
+    c.status()
+    assert int(c.lens[0]) == 1
+
+
+def test_the_library_without_a_status_word(tq_lib, cuda):
+    """d_status NULL: a page operation's own word tells, and nothing is held back."""
+    B = tq_lib.binding
+    c = make_cache(tq_lib, cuda, page=16, slots=2, max_pages=4, pages=2)
+    c.c.d_status = None
+    ws = torch.zeros(B.tq_kv8_workspace_bytes(B.TQ_KV8_OP_PAGES, c.c, 1, 0, 0, 0), dtype=torch.uint8, device=cuda)
+    stream = torch.cuda.current_stream().cuda_stream
+    slots, many, some = ints([0], cuda), ints([40], cuda), ints([20], cuda)
+    for counts, want in ((many, B.TQ_ERR_PAGES), (some, B.TQ_OK)):
+        B.tq_kv8_reserve(c.c, 1, slots.data_ptr(), counts.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+        assert B.lib.tq_device_status(ws.data_ptr(), stream) == want
+    assert c.lens.tolist() == [20, 0]
+    c.status()
+    x = torch.randn(20, 2, 128, device=cuda)
+    B.tq_kv8_append(c.c, 0, 1, slots.data_ptr(), cu_of([20], cuda).data_ptr(), 20, 20, x.data_ptr(),
+                    x.data_ptr(), B.TQ_F32, 256, 128, None, stream)
+    k, _ = c.read(0, ints([0], cuda), cu_of([20], cuda), 20, 20, dtype=torch.float32)
+    assert ((k - x).abs() <= x.abs().max() / 254 * 1.01).all()
