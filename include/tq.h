@@ -487,8 +487,9 @@ TQ_API int tq_kv8_compact(const tq_kv8_t *c, void *d_ws, size_t ws_bytes, void *
  * of x_dtype (TQ_F32, TQ_BF16, TQ_F16), strides in elements.  With r (may be
  * NULL) the keys are turned to their positions on the way, unrounded.  For
  * every page and head: s = max(s0, max|x| / M), s0 the scale of the tokens that
- * the page holds already (if any) and M = 127 or 448; codes = x / s rounded to
- * nearest even; where s > s0 the codes there are rounded again for s.  NaN
+ * the page holds already (if any) and M = 127 or 448 (the quotient rounded up where
+ * it lies below fp32's normal range); codes = x / s rounded to nearest even, x times
+ * the reciprocal of s in fp32; where s > s0 the codes there are rounded again for s.  NaN
  * counts as 0, a magnitude above 2^127 (an infinity) as 2^127.  A slot given twice, or slots
  * that share a page to be written (tq_kv8_reserve leaves none), is not
  * supported: the page's contents are then undefined. */

@@ -1,7 +1,8 @@
 // The 8-bit paged KV cache: geometry, writing tokens and reading them back.
 //
 // Write (tq_kv8_append): for every page and head that new tokens fall into,
-//   s = max(s0, max |x| / M)   (s0: the scale of the tokens there already, if any)
+//   s = max(s0, max |x| / M)   (s0: the scale of the tokens there already, if any;
+//                               below fp32's normal range the quotient is rounded up)
 //   code = rnd(x / s),         old codes: rnd(code s0 / s) where s > s0,
 // keys turned to their positions first (fp32, not rounded in between).
 //
@@ -221,17 +222,19 @@ __global__ __launch_bounds__(VEC == 8 ? 1024 : 256) void k_append(
         const uint32_t lane = threadIdx.x & 31;
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < blockDim.x / 32 ? red[lane] : 0u));
         if (held) return;  // (before the first store)
-        const float s = fmaxf(s_old, __fdiv_rn(top, code_max<FMT>()));
-        if (threadIdx.x == 0) a.scale[kv][ph] = s;
-        // (below fp32's normal range a reciprocal may overflow: all times 2^64)
-        const float up = s < 1.17549435e-38f ? 18446744073709551616.f : 1.f;
-        const float inv = s > 0.f ? __frcp_rn(s * up) : 0.f;
-        if (up != 1.f) {
+        float s = fmaxf(s_old, __fdiv_rn(top, code_max<FMT>()));
+        float up = 1.f;
+        if (s < 1.17549435e-38f) {  // below fp32's normal range:
+            // a few units of 2^-149 are rounded up, so that no code leaves its range;
+            if (fmaf(s, code_max<FMT>(), -top) < 0.f) s = __uint_as_float(__float_as_uint(s) + 1);
+            up = 18446744073709551616.f;  // a reciprocal may overflow: all times 2^64
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
                 for (int e = 0; e < 2 * VEC; ++e) val[i][e] *= up;
         }
+        if (threadIdx.x == 0) a.scale[kv][ph] = s;
+        const float inv = s > 0.f ? __frcp_rn(s * up) : 0.f;
         uint8_t* codes = a.codes[kv] + (ph << v.page_log2) * v.d;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {

@@ -114,7 +114,7 @@ __host__ __device__ constexpr float code_max() { return FMT == TQ_KV_I8 ? 127.f 
 // The nearest codes of four quotients x / s (ties to even): x times the fp32
 // reciprocal, off by 2^-23 of itself, so a code differs from the exact quotient's
 // only where that lies as close to the middle between two codes.  |x| <= s
-// code_max, so that nothing saturates.
+// code_max but for 2^-24 of it, so that nothing leaves the codes' range.
 template <int FMT>
 __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float inv) {
     if (FMT == TQ_KV_I8) {
