@@ -492,7 +492,9 @@ TQ_API int tq_kv8_compact(const tq_kv8_t *c, void *d_ws, size_t ws_bytes, void *
  * the reciprocal of s in fp32; where s > s0 the codes there are rounded again for s.  NaN
  * counts as 0, a magnitude above 2^127 (an infinity) as 2^127.  A slot given twice, or slots
  * that share a page to be written (tq_kv8_reserve leaves none), is not
- * supported: the page's contents are then undefined. */
+ * supported: the page's contents are then undefined.  An entry of more than max_new
+ * tokens, or a cu beyond total, leaves TQ_ERR_ARG in c->d_status; that entry's tokens
+ * are not written, the others' may not be. */
 TQ_API int tq_kv8_append(const tq_kv8_t *c, int layer, int ns, const int32_t *d_slots,
                          const int32_t *d_cu, int64_t total, int max_new, const void *d_k,
                          const void *d_v, int x_dtype, int64_t x_ts, int64_t x_hs,
@@ -519,7 +521,9 @@ TQ_API int tq_kv8_read(const tq_kv8_t *c, int layer, int ns, const int32_t *d_sl
  * (else TQ_ERR_UNSUPPORTED).
  * d_ws: >= tq_kv8_workspace_bytes(TQ_KV8_OP_ATTENTION, c, ns, total_q, max_q,
  * heads_q), any contents; calls that overlap on the GPU need workspaces of their
- * own.  The result does not depend on what else runs, nor on earlier calls.  A
+ * own.  A cu beyond total_q, or an entry of more than max_q tokens where max_q tokens
+ * have 16 rows at most (tokens x group), refuses the call: TQ_ERR_ARG in d_ws and
+ * c->d_status, every row as one that sees no key.  The result does not depend on what else runs, nor on earlier calls.  A
  * captured call that has timed out is to be captured anew. */
 TQ_API int tq_kv8_attention(const tq_kv8_t *c, int layer, int ns, const int32_t *d_slots,
                             const int32_t *d_cu, int64_t total_q, int max_q, int heads_q,

@@ -52,6 +52,7 @@ struct AppendArgs {
     const int32_t* cu;
     int ppb;  // pages a slot's new tokens can touch
     int hb;   // heads a block
+    int max_new;
     int64_t total;
     const void *x[2];
     int64_t x_ts, x_hs;
@@ -96,6 +97,10 @@ __global__ __launch_bounds__(VEC == 8 ? 1024 : 256) void k_append(
     const int64_t c0 = max(a.cu[seq], 0);
     const int count = (int)(min((int64_t)a.cu[seq + 1], a.total) - c0);
     if (slot < 0 || count <= 0) return;
+    if (count > a.max_new || a.cu[seq + 1] > a.total) {  // not what the host launched for
+        if (threadIdx.x == 0) leave_status(v, TQ_ERR_ARG);
+        return;
+    }
     const int len = length_of(v, slot);
     // tokens before the slot's first position have no place
     const int start = max(len - count, 0), skip = max(count - len, 0);
@@ -455,6 +460,7 @@ extern "C" int tq_kv8_append(const tq_kv8_t* c, int layer, int ns, const int32_t
     a.cu = d_cu;
     a.ppb = (int)(((int64_t)max_new + c->page - 2) / c->page + 1);
     if (a.ppb > c->max_pages) a.ppb = c->max_pages;
+    a.max_new = max_new;
     a.total = total;
     a.x[0] = d_k;
     a.x[1] = d_v;

@@ -300,7 +300,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         prefetch_tmap(&vmap);
     }
     grid_begin();
-    const int held = pending(a.v);
+    int held = pending(a.v);
     // (blocks are dispatched in order, and one that gives up has waited for a second)
     if (blockIdx.x == 0 && threadIdx.x == 0) *parts.status = held;
 
@@ -311,6 +311,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         int items = 0, most = 0;
         for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i) {
             const Span s = span_of(a, i);
+            if (misfit(a, i, s.e)) held = held ? held : TQ_ERR_ARG;
             steps += s.steps;
             items = min(items + (s.steps > 0 ? a.v.heads : 0), 1 << 20);
             most = max(most, s.steps > 0 ? s.tiles : 0);
@@ -331,6 +332,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             sm.warp_most[warp] = most;
         }
         if (__syncthreads_or(held)) {
+            if (blockIdx.x == 0 && held == TQ_ERR_ARG) {
+                *parts.status = held;
+                leave_status(a.v, held);
+            }
             empty_rows<D, T>(a);
             return;
         }
@@ -969,6 +974,7 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
     cudaStream_t s = (cudaStream_t)stream;
     const bool few = kv8::any_few(c, ns, total_q, max_q, heads_q);
     const int64_t most = (int64_t)max_q * a.group;
+    a.max_q = kv8::any_many(c, max_q, heads_q) ? INT32_MAX : max_q;
     a.few = few ? (int)(most < kv8::kRows ? most : kv8::kRows) : 0;
     size_t at = 256;
     if (few) {

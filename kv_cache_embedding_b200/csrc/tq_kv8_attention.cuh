@@ -23,6 +23,7 @@ struct Attn {
     void* out;
     float* lse;
     int rows;  // rows of the layer's pools: pages * heads * page
+    int max_q; // tokens of an entry at most, where the prompt kernel is not launched
     int few;   // entries of up to `few` query rows (tokens x group) run on the few-rows
                // kernel, the others on the prompt kernel (0: all of them)
 };
@@ -64,8 +65,14 @@ __device__ __forceinline__ Entry entry_of(const Attn& a, int i) {
     e.len = e.slot >= 0 ? length_of(a.v, e.slot) : 0;
     return e;
 }
-// A call that finds the cache's status set: no row sees a key.  (All of the grid's
-// threads; a block that saw the word before it was set may write rows too.)
+// A batch that does not fit the call's sizes, which the host cannot see: more tokens
+// than q has, or an entry that none of the launched kernels takes.
+__device__ __forceinline__ bool misfit(const Attn& a, int i, const Entry& e) {
+    return a.cu[i + 1] > a.total_q || e.qn > a.max_q;
+}
+
+// A refused call, or one that finds the cache's status set: no row sees a key.  (All of
+// the grid's threads; a block that saw the word before it was set may write rows too.)
 template <int D, typename T>
 __device__ __forceinline__ void empty_rows(const Attn& a) {
     const int64_t t0 = max(a.cu[0], 0), rows = (min((int64_t)a.cu[a.ns], a.total_q) - t0) * a.heads_q;

@@ -157,16 +157,22 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
     const int run = (a.ns + kPThreads - 1) / kPThreads;
     {
         int64_t mine = 0;
+        bool bad = false;
         if (a.ns <= 32) {
             for (int i = warp; i < a.ns; i += kPThreads / 32) {
-                const int64_t n = warp_sum(tiles_per_head(a, entry_of(a, i), lane, 32));
+                const Entry e = entry_of(a, i);
+                bad |= misfit(a, i, e);
+                const int64_t n = warp_sum(tiles_per_head(a, e, lane, 32));
                 if (lane == 0) pre[kPThreads + 1 + i] = a.v.heads * n;
             }
             __syncthreads();
             if ((int)threadIdx.x < a.ns) mine = pre[kPThreads + 1 + threadIdx.x];
         } else {
-            for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i)
-                mine += a.v.heads * tiles_per_head(a, entry_of(a, i), 0, 1);
+            for (int i = threadIdx.x * run; i < min(a.ns, (int)(threadIdx.x + 1) * run); ++i) {
+                const Entry e = entry_of(a, i);
+                bad |= misfit(a, i, e);
+                mine += a.v.heads * tiles_per_head(a, e, 0, 1);
+            }
         }
         if (threadIdx.x == 0) {
             sm.abort = 0;
@@ -203,8 +209,9 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
         }
         int64_t* sums = pre + kPThreads + 40;
         if (lane == 31) sums[warp] = inc;
-        if (__syncthreads_or(threadIdx.x == 0 && pending(a.v))) {  // (k_prompt_merge writes the rows)
-            if (threadIdx.x == 0) parts.block_status[unit] = 0;
+        bad = __syncthreads_or(bad);
+        if (__syncthreads_or(bad || (threadIdx.x == 0 && pending(a.v)))) {  // (k_prompt_merge writes the rows)
+            if (threadIdx.x == 0) parts.block_status[unit] = bad ? TQ_ERR_ARG : 0;
             return;
         }
         for (int w = 0; w < warp; ++w) inc += sums[w];
@@ -765,25 +772,26 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
 }
 
 // Joins the parts of the items that were cut: blocks (u, y) the item that begins
-// in CTA u, a warp a row, 4 coordinates a lane (d = 128) or 2.  With the cache's status
-// set it writes the rows of a call that saw no key.
+// in CTA u, a warp a row, 4 coordinates a lane (d = 128) or 2.  Where the call was
+// refused or the cache's status is set it writes rows that see no key.
 template <int D, typename T>
 __global__ __launch_bounds__(256) void k_prompt_merge(const Attn a, const PromptParts parts, int blocks) {
     const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_begin();
+    const bool bad = parts.block_status[0] == TQ_ERR_ARG;  // (all blocks', then)
     const int held = pending(a.v);
     if (u == 0 && blockIdx.y == 0) {
         int st = 0;
         for (int i = threadIdx.x; i < blocks; i += 256) st |= parts.block_status[i] != 0;
         st = __syncthreads_or(st);
-        const int status = st ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 81 : held;
+        const int status = bad ? TQ_ERR_ARG : st ? TQ_ERR_DEVICE_TIMEOUT * 1000 - 81 : held;
         // (the few-rows kernel of the call has set the word; a time-out stands)
         if (threadIdx.x == 0 && (st || !parts.keep_status)) *parts.status = status;
         if (threadIdx.x == 0 && st) leave_status(a.v, status);
     }
     const Cut c = parts.cut[u];
-    if (held) empty_rows<D, T>(a);
-    if (held || c.parts == 0) return;
+    if (held || bad) empty_rows<D, T>(a);
+    if (held || bad || c.parts == 0) return;
     constexpr int E = D / 32;
     auto slot = [&](int i) { return i == 0 ? 2 * (int64_t)u + 1 : 2 * (int64_t)(u + i); };
     for (int r = blockIdx.y * 8 + warp; r < c.rows; r += gridDim.y * 8) {

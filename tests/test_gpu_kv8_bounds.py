@@ -11,6 +11,56 @@ from tests.test_gpu_kv8 import (PEAK, assert_near, check_attention, cu_of, dense
 pytestmark = pytest.mark.gpu
 
 
+def refused(tq_lib, c):
+    with pytest.raises(tq_lib.TQError) as e:
+        c.status()
+    assert e.value.status == tq_lib.binding.TQ_ERR_ARG
+    c.status()
+
+
+def dirty(n):
+    """Memory that a call may be handed holds anything."""
+    torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("counts,max_q", [([1, 7], 1), ([2, 1], 1), ([5, 300], 4)])
+def test_attention_counts_above_max_q(tq_lib, cuda, counts, max_q):
+    """Computed all the same, or refused: never left as the memory was."""
+    lens = [90, 400]
+    c = fill(tq_lib, cuda, "i8", 2, 128, 32, lens)
+    q = torch.randn(sum(counts), 8, 128, generator=gen(1)).to(torch.bfloat16).to(cuda)
+    dirty(q.numel() * 2)
+    lse = torch.full((sum(counts), 8), 7.0, device=cuda)
+    out = c.attention(0, q, cu_of(counts, cuda), max_q, lse=lse)
+    assert not (out.view(torch.int16) == 0x7F7F).any()
+    refused(tq_lib, c)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    check_attention(c, q, counts, lens)  # and afterwards it works
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [40, 60]])
+def test_attention_counts_beyond_q(tq_lib, cuda, counts):
+    """cu that names more tokens than q has: refused."""
+    lens = [90, 400]
+    c = fill(tq_lib, cuda, "i8", 2, 128, 32, lens)
+    q = torch.randn(sum(counts) - 1, 8, 128, generator=gen(1)).to(torch.bfloat16).to(cuda)
+    out = c.attention(0, q, cu_of(counts, cuda), max(counts))
+    refused(tq_lib, c)
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("counts,max_new,short", [([40, 3], 3, 0), ([2, 1], 1, 0), ([3, 5], 5, 1)])
+def test_append_counts_above_max_new(tq_lib, cuda, counts, max_new, short):
+    """More tokens than the host said, or than k has: refused, and later calls wait
+    for status()."""
+    c = make_cache(tq_lib, cuda, page=16, slots=2, max_pages=4, pages=8)
+    c.reserve(ints([0, 1], cuda), ints(counts, cuda))
+    c.status()
+    x = torch.randn(sum(counts) - short, 2, 128, device=cuda).to(torch.bfloat16)
+    c.append(0, x, x, cu_of(counts, cuda), max_new)
+    refused(tq_lib, c)
+
+
 @pytest.mark.parametrize("fmt", ["i8", "e4m3"])
 def test_append_tiny_values(tq_lib, cuda, fmt):
     """Maxima down to fp32's last bit, where max / M is a few units of 2^-149 itself:
