@@ -502,7 +502,8 @@ TQ_API int tq_kv8_append(const tq_kv8_t *c, int layer, int ns, const int32_t *d_
 
 /* Reads tokens d_begin[i] .. d_begin[i] + cu[i+1] - cu[i] of every slot back:
  * d_k, d_v [total][heads][d] of dtype (either may be NULL), 0 beyond the slot's
- * length or before its start. */
+ * length or before its start, and in the rows behind cu[ns].  max_new sizes the
+ * launch: entries of more tokens are read as well, only slower. */
 TQ_API int tq_kv8_read(const tq_kv8_t *c, int layer, int ns, const int32_t *d_slots,
                        const int32_t *d_begin, const int32_t *d_cu, int64_t total, int max_new,
                        void *d_k, void *d_v, int dtype, void *stream);

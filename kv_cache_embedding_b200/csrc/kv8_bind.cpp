@@ -319,9 +319,11 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor out[2];
     for (at::Tensor& o : out)
         o = at::detail::empty_cuda({total, c->c.heads, c->c.d}, t, c->device, std::nullopt);
+    const int max_count = int32(a[5], "max_count");
+    if (b.ns == 0 || max_count == 0)  // (no launch)
+        for (at::Tensor& o : out) o.zero_();
     check("tq_kv8_read", tq_kv8_read(&c->c, int32(a[1], "layer"), b.ns, b.slots, begin, b.cu, total,
-                                     int32(a[5], "max_count"), out[0].data_ptr(), out[1].data_ptr(),
-                                     code_of(t),
+                                     max_count, out[0].data_ptr(), out[1].data_ptr(), code_of(t),
                                      c10::cuda::getCurrentCUDAStream(c->device.index()).stream()));
     PyObject* pair = PyTuple_New(2);
     if (!pair) throw Fail();

@@ -334,74 +334,85 @@ constexpr int kReadThreads = 256;
 constexpr int kReadItems = 4;  // of 16 codes, a thread
 
 // A block reads `tokens` tokens of one slot, all heads, K or V: 16 codes an item.
-// The lookups of a thread's items, then their codes, are on their way together.
+// (and, of an entry with more tokens than the launch was sized for, every bps-th such
+// run behind it).  The lookups of a thread's items, then their codes, are on their way
+// together.  Rows that no entry owns become 0.
 // Bound by HBM: 28306 tokens x 8 heads of 128, e4m3 to bf16, 38 us, 4.6 TB/s.
 template <typename T, int FMT>
 __global__ __launch_bounds__(kReadThreads) void k_read(View v, const int32_t* slots, const int32_t* begin,
-                                                       const int32_t* cu, int bps, int tokens, int64_t total,
+                                                       const int32_t* cu, int ns, int bps, int tokens, int64_t total,
                                                        const uint8_t* kc, const uint8_t* vc, const float* ks,
                                                        const float* vs, T* out_k, T* out_v) {
     grid_begin();
     const int seq = blockIdx.x / bps, blk = blockIdx.x - seq * bps;
     const int slot = slot_of(v, slots, seq);
     const int64_t c0 = max(cu[seq], 0), c1 = min((int64_t)cu[seq + 1], total);
-    const int64_t b = (int64_t)begin[seq] + (int64_t)blk * tokens;
+    const int used = max(cu[ns], 0);
+    const int64_t b0 = begin[seq];
     const int held = v.status ? *v.status : 0;  // (through L1: nothing here has to agree on it)
     int len = slot >= 0 ? length_of(v, slot) : 0;
     if (held) len = 0;
-    const int nt = (int)min((int64_t)tokens, c1 - c0 - (int64_t)blk * tokens);
-    if (nt <= 0) return;
-    const int chunks = v.d / 16, per = v.heads * chunks, n = nt * per;
+    const int chunks = v.d / 16, per = v.heads * chunks;
     const bool is_v = blockIdx.y != 0;
     T* out = is_v ? out_v : out_k;
     if (!out) return;
     const uint8_t* codes = is_v ? vc : kc;
     const float* scales = is_v ? vs : ks;
-    // (items of a block are neighbours in the output: token, head, chunk)
-    Pack<T, 8>* dst = reinterpret_cast<Pack<T, 8>*>(out + (c0 + (int64_t)blk * tokens) * v.heads * v.d);
-    for (int i0 = threadIdx.x; i0 < n; i0 += kReadItems * kReadThreads) {
-        int pid[kReadItems];
+    for (int64_t first = (int64_t)blk * tokens; first < c1 - c0; first += (int64_t)bps * tokens) {
+        const int64_t b = b0 + first;
+        const int n = (int)min((int64_t)tokens, c1 - c0 - first) * per;
+        // (items of a block are neighbours in the output: token, head, chunk)
+        Pack<T, 8>* dst = reinterpret_cast<Pack<T, 8>*>(out + (c0 + first) * v.heads * v.d);
+        for (int i0 = threadIdx.x; i0 < n; i0 += kReadItems * kReadThreads) {
+            int pid[kReadItems];
 #pragma unroll
-        for (int e = 0; e < kReadItems; ++e) {
-            const int i = i0 + e * kReadThreads;
-            pid[e] = -1;
-            if (i < n) {
-                const int64_t pos = b + i / per;
-                if (pos >= 0 && pos < len) pid[e] = page_of(v, slot, (int)(pos >> v.page_log2));
+            for (int e = 0; e < kReadItems; ++e) {
+                const int i = i0 + e * kReadThreads;
+                pid[e] = -1;
+                if (i < n) {
+                    const int64_t pos = b + i / per;
+                    if (pos >= 0 && pos < len) pid[e] = page_of(v, slot, (int)(pos >> v.page_log2));
+                }
             }
-        }
-        uint4 w[kReadItems];
-        float s[kReadItems];
+            uint4 w[kReadItems];
+            float s[kReadItems];
 #pragma unroll
-        for (int e = 0; e < kReadItems; ++e) {
-            const int i = i0 + e * kReadThreads;
-            w[e] = make_uint4(0, 0, 0, 0);
-            s[e] = 0.f;
-            if (pid[e] >= 0) {
-                const int t = i / per, hc = i - t * per, h = hc / chunks, ch = hc - h * chunks;
-                const int64_t ph = (int64_t)pid[e] * v.heads + h;
-                w[e] = *reinterpret_cast<const uint4*>(
-                    codes + ((ph << v.page_log2) + ((b + t) & (v.page - 1))) * v.d + 16 * ch);
-                s[e] = scales[ph];
+            for (int e = 0; e < kReadItems; ++e) {
+                const int i = i0 + e * kReadThreads;
+                w[e] = make_uint4(0, 0, 0, 0);
+                s[e] = 0.f;
+                if (pid[e] >= 0) {
+                    const int t = i / per, hc = i - t * per, h = hc / chunks, ch = hc - h * chunks;
+                    const int64_t ph = (int64_t)pid[e] * v.heads + h;
+                    w[e] = *reinterpret_cast<const uint4*>(
+                        codes + ((ph << v.page_log2) + ((b + t) & (v.page - 1))) * v.d + 16 * ch);
+                    s[e] = scales[ph];
+                }
             }
-        }
 #pragma unroll
-        for (int e = 0; e < kReadItems; ++e) {
-            const int i = i0 + e * kReadThreads;
-            if (i >= n) continue;
-            const uint32_t ww[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
-            Pack<T, 8> o[2];
+            for (int e = 0; e < kReadItems; ++e) {
+                const int i = i0 + e * kReadThreads;
+                if (i >= n) continue;
+                const uint32_t ww[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+                Pack<T, 8> o[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float x[4];
-                decode4<FMT>(ww[k], x);
+                for (int k = 0; k < 4; ++k) {
+                    float x[4];
+                    decode4<FMT>(ww[k], x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) from_f(s[e] * x[j], o[k / 2].v[4 * (k & 1) + j]);
+                    for (int j = 0; j < 4; ++j) from_f(s[e] * x[j], o[k / 2].v[4 * (k & 1) + j]);
+                }
+                dst[2 * (int64_t)i] = o[0];
+                dst[2 * (int64_t)i + 1] = o[1];
             }
-            dst[2 * (int64_t)i] = o[0];
-            dst[2 * (int64_t)i + 1] = o[1];
         }
     }
+    Pack<T, 8> zero;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) from_f(0.f, zero.v[j]);
+    for (int64_t t = (int64_t)used + blockIdx.x; t < total; t += gridDim.x)
+        for (int i = threadIdx.x; i < 2 * per; i += kReadThreads)
+            reinterpret_cast<Pack<T, 8>*>(out + t * v.heads * v.d)[i] = zero;
 }
 
 template <typename T>
@@ -420,7 +431,7 @@ int read_type(const tq_kv8_t* c, int layer, int ns, const int32_t* slots, const 
     const float* ks = c->d_kscale + layer * layer_scales(c);
     const float* vs = c->d_vscale + layer * layer_scales(c);
     return launch_behind(c->format == TQ_KV_I8 ? k_read<T, TQ_KV_I8> : k_read<T, TQ_KV_E4M3>, grid,
-                         kReadThreads, 0, s, view(c), slots, begin, cu, (int)bps, (int)tokens, total, kc, vc,
+                         kReadThreads, 0, s, view(c), slots, begin, cu, ns, (int)bps, (int)tokens, total, kc, vc,
                          ks, vs, (T*)k, (T*)v);
 }
 

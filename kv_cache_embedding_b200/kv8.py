@@ -151,7 +151,9 @@ class KV8Cache:
         N.append(self._h, layer, k, v, cu, max_new, slots, None if rope is None else rope._h)
 
     def read(self, layer, begin, cu, total, max_count, slots=None, dtype=torch.bfloat16):
-        """(k, v) [total, heads, d] of tokens begin[i] .. begin[i] + cu[i+1] - cu[i]."""
+        """(k, v) [total, heads, d] of tokens begin[i] .. begin[i] + cu[i+1] - cu[i]
+        (max_count: as many at most, a hint); 0 where there is no such token, and
+        behind cu[-1]."""
         return N.read(self._h, layer, begin, cu, total, max_count, slots, dtype)
 
     def attention(self, layer, q, cu, max_q, slots=None, scale=None, causal=True, window=0,

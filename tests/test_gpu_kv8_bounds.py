@@ -61,6 +61,28 @@ def test_append_counts_above_max_new(tq_lib, cuda, counts, max_new, short):
     refused(tq_lib, c)
 
 
+@pytest.mark.parametrize("max_count", [1, 7, 40])
+def test_read_more_than_max_count(tq_lib, cuda, max_count):
+    """Every token that cu names is read, and rows behind them are 0."""
+    lens = [90, 33]
+    c = fill(tq_lib, cuda, "e4m3", 2, 64, 16, lens)
+    counts, begin, total = [60, 33], [20, 0], 130
+    want = [torch.cat([values(c, name, 0, i, b + n)[:, b:].transpose(0, 1)
+                       for i, (b, n) in enumerate(zip(begin, counts))]) for name in "kv"]
+    dirty(total * 2 * 64 * 4)
+    dirty(total * 2 * 64 * 4)
+    got = c.read(0, ints(begin, cuda), cu_of(counts, cuda), total, max_count, dtype=torch.float32)
+    for g, w in zip(got, want):
+        assert ((g[:93].cpu().double() - w).abs() <= w.abs() * 2.0 ** -23).all()
+        assert (g[93:] == 0).all()
+    for cu, most in (([0], 4), ([0, 0, 0], 0)):
+        dirty(total * 2 * 64 * 4)
+        dirty(total * 2 * 64 * 4)
+        n = len(cu) - 1
+        got = c.read(0, ints(begin[:n], cuda), ints(cu, cuda), total, most, dtype=torch.float32)
+        assert all((g == 0).all() for g in got)
+
+
 @pytest.mark.parametrize("fmt", ["i8", "e4m3"])
 def test_append_tiny_values(tq_lib, cuda, fmt):
     """Maxima down to fp32's last bit, where max / M is a few units of 2^-149 itself:
