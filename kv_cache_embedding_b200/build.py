@@ -29,7 +29,8 @@ def _stale():
     if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    deps = [BIND_SRC] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "tq.h")]
+    deps = [BIND_SRC] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    deps.append(os.path.join(INCLUDE, "tq.h"))
     return any(os.path.getmtime(p) > t for p in deps)
 
 

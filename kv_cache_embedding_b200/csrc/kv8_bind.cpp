@@ -20,7 +20,7 @@
 
 #include <unordered_map>
 
-#include "tq.h"
+#include "kv8_bind.h"
 
 namespace {
 
@@ -364,6 +364,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         lse = (float*)l.data_ptr();
     }
     const Batch b = batch(c, a[5], a[3]);
+    const bool fresh = a[9] == Py_None;
     double scale = 0.0;
     if (a[6] == Py_None) {
         scale = c->c.d == 64 ? 0.125 : 0.08838834764831845;  // 1 / sqrt(d)
@@ -378,10 +379,12 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Ws w = {nullptr, 0, {}};
     if (max_q >= 0 && heads_q >= 1 && heads_q % c->c.heads == 0)
         w = workspace(c, TQ_KV8_OP_ATTENTION, b.ns, total, max_q, (int)heads_q, s);
+    if (fresh && (b.ns == 0 || max_q == 0)) out.zero_();  // (no launch)
     check("tq_kv8_attention",
-          tq_kv8_attention(&c->c, layer, b.ns, b.slots, b.cu, total, max_q, (int)heads_q, q.data_ptr(),
-                           code_of(q.scalar_type()), q.stride(0), q.stride(1), (float)scale, causal,
-                           window, out.data_ptr(), lse, w.ptr, w.bytes, s));
+          tq_kv8_attention_rows(&c->c, layer, b.ns, b.slots, b.cu, total, max_q, (int)heads_q,
+                                q.data_ptr(), code_of(q.scalar_type()), q.stride(0), q.stride(1),
+                                (float)scale, causal, window, out.data_ptr(), fresh, lse, w.ptr,
+                                w.bytes, s));
     return THPVariable_Wrap(std::move(out));
     TQ_PY_END
 }

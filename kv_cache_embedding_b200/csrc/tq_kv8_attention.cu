@@ -33,6 +33,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "kv8_bind.h"
 #include "tq_kv8_attention.cuh"
 
 namespace tq {
@@ -133,6 +134,7 @@ struct Smem {
     Job job[kWarps + 1];                 // of the items that a warp begins; the last: begun before the block
     int outside[kWarps];                 // this warp left the end of an item in the workspace
     int beyond;                          // an item goes on behind the block
+    int used;                            // tokens that entries own
     int abort;
 };
 
@@ -293,6 +295,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         sm.job[kWarps].parts = 0;
         sm.outside[warp] = 0;
     }
+    if (threadIdx.x == 64) sm.used = INT32_MAX;
     if (lane < NS) mbar_init(&sm.full[warp][lane], 1);
     fence_mbar_init();
     if (threadIdx.x == 0) {
@@ -301,6 +304,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     }
     grid_begin();
     int held = pending(a.v);
+    if (a.behind && threadIdx.x == 64) sm.used = max(a.cu[a.ns], 0);
     // (blocks are dispatched in order, and one that gives up has waited for a second)
     if (blockIdx.x == 0 && threadIdx.x == 0) *parts.status = held;
 
@@ -337,6 +341,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                 leave_status(a.v, held);
             }
             empty_rows<D, T>(a);
+            zero_behind<D, T>(a, sm.used);
             return;
         }
         for (int w = 0; w < warp; ++w) {
@@ -833,6 +838,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             }
         }
     }
+    if (sm.used < a.total_q) zero_behind<D, T>(a, sm.used);
     if (threadIdx.x == 0 && sm.abort) {
         *parts.status = TQ_ERR_DEVICE_TIMEOUT * 1000 - 80;
         leave_status(a.v, TQ_ERR_DEVICE_TIMEOUT * 1000 - 80);
@@ -936,6 +942,15 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
                                 const void* d_q, int q_dtype, int64_t q_ts, int64_t q_hs, float scale,
                                 int causal, int window, void* d_out, float* d_lse, void* d_ws,
                                 size_t ws_bytes, void* stream) {
+    return tq_kv8_attention_rows(c, layer, ns, d_slots, d_cu, total_q, max_q, heads_q, d_q, q_dtype, q_ts,
+                                 q_hs, scale, causal, window, d_out, 0, d_lse, d_ws, ws_bytes, stream);
+}
+
+extern "C" int tq_kv8_attention_rows(const tq_kv8_t* c, int layer, int ns, const int32_t* d_slots,
+                                     const int32_t* d_cu, int64_t total_q, int max_q, int heads_q,
+                                     const void* d_q, int q_dtype, int64_t q_ts, int64_t q_hs, float scale,
+                                     int causal, int window, void* d_out, int zero_behind, float* d_lse,
+                                     void* d_ws, size_t ws_bytes, void* stream) {
     int status;
     if (!kv8::valid(c, &status)) return status;
     if (layer < 0 || layer >= c->layers || ns < 0 || total_q < 0 || max_q < 0 || heads_q < 1)
@@ -969,6 +984,7 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
     a.ks = c->d_kscale + layer * kv8::layer_scales(c);
     a.vs = c->d_vscale + layer * kv8::layer_scales(c);
     a.out = d_out;
+    a.behind = zero_behind;
     a.lse = d_lse;
     a.rows = c->pages * c->heads * c->page;
     cudaStream_t s = (cudaStream_t)stream;
@@ -991,6 +1007,7 @@ extern "C" int tq_kv8_attention(const tq_kv8_t* c, int layer, int ns, const int3
         if (rc) return rc;
     }
     if (!kv8::any_many(c, max_q, heads_q)) return TQ_OK;
+    if (few) a.behind = 0;  // (done)
     size_t bytes;
     const int blocks = kv8::prompt_blocks(c, ns, total_q, heads_q);
     kv8::PromptParts p = kv8::prompt_carve(c, (char*)d_ws + at, blocks, &bytes);

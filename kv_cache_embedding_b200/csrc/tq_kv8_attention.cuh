@@ -22,6 +22,7 @@ struct Attn {
     const float *ks, *vs;  // [pages][heads] of the layer
     void* out;
     float* lse;
+    int behind;  // rows behind the last entry's become 0
     int rows;  // rows of the layer's pools: pages * heads * page
     int max_q; // tokens of an entry at most, where the prompt kernel is not launched
     int few;   // entries of up to `few` query rows (tokens x group) run on the few-rows
@@ -82,6 +83,15 @@ __device__ __forceinline__ void empty_rows(const Attn& a) {
     for (int64_t i = at; i < rows * (D / 8); i += step) out[i] = make_uint4(0, 0, 0, 0);
     if (a.lse)
         for (int64_t i = at; i < rows; i += step) a.lse[t0 * a.heads_q + i] = -INFINITY;
+}
+
+// Rows behind the last entry's (all of the grid's threads; the first kernel of a call).
+template <int D, typename T>
+__device__ __forceinline__ void zero_behind(const Attn& a, int used) {
+    const int64_t row = (int64_t)a.heads_q * (D / 8);  // 16-byte pieces of a token
+    const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+    uint4* out = reinterpret_cast<uint4*>(a.out);
+    for (int64_t i = used * row + at; i < a.total_q * row; i += step) out[i] = make_uint4(0, 0, 0, 0);
 }
 
 // First key that any query of the entry sees.

@@ -773,11 +773,13 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
 
 // Joins the parts of the items that were cut: blocks (u, y) the item that begins
 // in CTA u, a warp a row, 4 coordinates a lane (d = 128) or 2.  Where the call was
-// refused or the cache's status is set it writes rows that see no key.
+// refused or the cache's status is set it writes rows that see no key; rows behind the
+// last entry's are its work too.
 template <int D, typename T>
 __global__ __launch_bounds__(256) void k_prompt_merge(const Attn a, const PromptParts parts, int blocks) {
     const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_begin();
+    if (a.behind && blockIdx.y == 0) zero_behind<D, T>(a, max(a.cu[a.ns], 0));
     const bool bad = parts.block_status[0] == TQ_ERR_ARG;  // (all blocks', then)
     const int held = pending(a.v);
     if (u == 0 && blockIdx.y == 0) {

@@ -83,6 +83,32 @@ def test_read_more_than_max_count(tq_lib, cuda, max_count):
         assert all((g == 0).all() for g in got)
 
 
+@pytest.mark.parametrize("counts,max_q", [([1, 1], 1), ([3, 1], 4), ([64, 30], 64), ([1, 100], 100)])
+def test_attention_rows_behind(tq_lib, cuda, counts, max_q):
+    """A padded q: the rows behind the last sequence's are 0 in an output that the
+    call allocates, and stay as they were in one that is given."""
+    lens = [90, 400]
+    c = fill(tq_lib, cuda, "i8", 2, 64, 32, lens)
+    used = sum(counts)
+    q = torch.randn(used + 37, 8, 64, generator=gen(1)).to(torch.bfloat16).to(cuda)
+    dirty(q.numel() * 2)
+    out = c.attention(0, q, cu_of(counts, cuda), max_q)
+    keep = torch.full_like(q, 3.0)
+    c.attention(0, q, cu_of(counts, cuda), max_q, out=keep)
+    c.status()
+    assert (out[used:] == 0).all() and (keep[used:] == 3.0).all()
+    assert torch.equal(out[:used], keep[:used])
+    at = 0
+    for i, (m, n) in enumerate(zip(counts, lens)):
+        ref, bound, _ = dense(q[at:at + m].cpu(), values(c, "k", 0, i, n), values(c, "v", 0, i, n),
+                              visible(m, n, True, 0), 64 ** -0.5)
+        assert_near(out[at:at + m], ref, bound)
+        at += m
+    for cu, most in (([0], 4), ([0, 0, 0], 0), ([0, 0, 0], max_q)):  # entries without tokens
+        dirty(q.numel() * 2)
+        assert (c.attention(0, q, ints(cu, cuda), most) == 0).all()
+
+
 @pytest.mark.parametrize("fmt", ["i8", "e4m3"])
 def test_append_tiny_values(tq_lib, cuda, fmt):
     """Maxima down to fp32's last bit, where max / M is a few units of 2^-149 itself:
