@@ -270,7 +270,7 @@ __device__ __forceinline__ void write_row(const Attn& a, const Job& job, int r, 
     for (int k = 0; k < E; ++k) from_f(s.acc[k] * n, y.v[k]);
     *reinterpret_cast<Pack<T, E>*>((T*)a.out + (tok * a.heads_q + hq) * D + lane * E) = y;
     if (a.lse && lane == 0)
-        a.lse[tok * a.heads_q + hq] = s.L > 0.f ? (s.m + log2f(s.L)) * 0.69314718056f : s.m;
+        a.lse[tok * a.heads_q + hq] = s.L > 0.f ? (s.m + log2f(s.L)) * 0.69314718056f : s.L == 0.f ? -INFINITY : s.L;
 }
 
 // NB: blocks of 8 query rows.
@@ -713,7 +713,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                     *reinterpret_cast<Pack<T, 2>*>(out + 16 * ch) = v;
                 }
                 if (a.lse && r0 == 0)
-                    a.lse[tok * a.heads_q + hq] = L[u] > 0.f ? (m[u] + log2f(L[u])) * 0.69314718056f : m[u];
+                    a.lse[tok * a.heads_q + hq] =
+                        L[u] > 0.f ? (m[u] + log2f(L[u])) * 0.69314718056f : L[u] == 0.f ? -INFINITY : L[u];
             } else {
                 if (r0 == 0) part_ml[r] = make_float2(m[u], L[u]);
                 float* dst = part_o + r * D + 2 * r0;

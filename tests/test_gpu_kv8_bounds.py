@@ -109,6 +109,25 @@ def test_attention_rows_behind(tq_lib, cuda, counts, max_q):
         assert (c.attention(0, q, ints(cu, cuda), most) == 0).all()
 
 
+@pytest.mark.parametrize("count", [1, 3, 40])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_lse_of_a_bad_query(tq_lib, cuda, count, bad):
+    """A row whose query is not finite: NaN, in the log sum as well; the others as
+    without it."""
+    c = fill(tq_lib, cuda, "i8", 1, 128, 64, [300])
+    q = torch.randn(count, 4, 128, generator=gen(1)).to(torch.bfloat16).to(cuda)
+    cu = cu_of([count], cuda)
+    good, lse0 = c.attention(0, q, cu, count, lse=(l := torch.zeros(count, 4, device=cuda))), l
+    q[count - 1, 2, 5] = bad
+    lse = torch.zeros(count, 4, device=cuda)
+    out = c.attention(0, q, cu, count, lse=lse)
+    c.status()
+    hit = torch.zeros(count, 4, dtype=torch.bool, device=cuda)
+    hit[count - 1, 2] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse[~hit], lse0[~hit])
+
+
 @pytest.mark.parametrize("fmt", ["i8", "e4m3"])
 def test_append_tiny_values(tq_lib, cuda, fmt):
     """Maxima down to fp32's last bit, where max / M is a few units of 2^-149 itself:
