@@ -9,6 +9,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -76,6 +77,14 @@ at::Tensor rows(PyObject* o, int64_t heads, int64_t d, const char* name) {
                      "; expected float32, bfloat16 or float16");
     TORCH_CHECK_VALUE(x.is_cuda(), name, ": expected a CUDA tensor, got one on ", x.device());
     return x.stride(2) == 1 ? x : x.contiguous();
+}
+
+// What is computed here has no derivative for torch to find.
+bool backward_grad(const at::Tensor& x) { return x.requires_grad() && c10::GradMode::is_enabled(); }
+bool wants_grad(const at::Tensor& x) { return backward_grad(x) || x._fw_grad(0).defined(); }
+void no_grad(const at::Tensor& x, const char* name, const char* call) {
+    TORCH_CHECK_VALUE(!wants_grad(x), name, ": ", call, " has no gradient; detach() the tensor, or call it under "
+                      "torch.no_grad()");
 }
 
 // A contiguous [n] index tensor.
@@ -181,12 +190,14 @@ PyObject* py_rope_params(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TQ_PY_END
 }
 
-// (rope, x, pos, out or None, transpose)
+// (rope, x, pos, out or None, transpose); None where the caller is to differentiate
 PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TQ_PY_BEGIN
     expect_args(n, 5);
     const tq_rope_params_t* r = rope_params(a[0]);
     const at::Tensor x = rows(a[1], -1, r->d, "x");
+    if (a[3] == Py_None && backward_grad(x)) Py_RETURN_NONE;
+    no_grad(x, "x", a[3] == Py_None ? "forward mode" : "a rotation into a given tensor");
     const int64_t T = x.size(0), heads = x.size(1);
     const int64_t* pos = ints<int64_t>(a[2], "pos", T, x.device());
     const c10::cuda::CUDAGuard guard(x.device());
@@ -195,6 +206,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         out = at::detail::empty_cuda(x.sizes(), x.scalar_type(), x.device(), std::nullopt);
     } else {
         out = tensor(a[3], "out");
+        no_grad(out, "out", "a rotation into a given tensor");
         TORCH_CHECK_VALUE(out.sizes() == x.sizes() && out.scalar_type() == x.scalar_type() &&
                               out.device() == x.device() && out.stride(2) == 1,
                           "out: expected x's shape, type and device, contiguous heads");
@@ -288,6 +300,8 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type() &&
                           k.device() == c->device && v.device() == c->device,
                       "k, v: expected one shape and type, on the cache's device");
+    no_grad(k, "k", "append");
+    no_grad(v, "v", "append");
     const c10::cuda::CUDAGuard guard(c->device);
     if (k.strides() != v.strides()) {
         k = k.contiguous();
@@ -340,6 +354,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Cache* c = cache(a[0]);
     at::Tensor q = rows(a[2], -1, c->c.d, "q");
     TORCH_CHECK_VALUE(q.device() == c->device, "q: expected a tensor on ", c->device);
+    no_grad(q, "q", "attention over the cache");
     const int64_t total = q.size(0), heads_q = q.size(1);
     TORCH_CHECK_VALUE(heads_q <= INT32_MAX, "q: too many heads");
     const c10::cuda::CUDAGuard guard(c->device);
@@ -350,6 +365,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         out = at::detail::empty_cuda(q.sizes(), q.scalar_type(), c->device, std::nullopt);
     } else {
         out = tensor(a[9], "out");
+        no_grad(out, "out", "attention over the cache");
         TORCH_CHECK_VALUE(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type() &&
                               out.device() == c->device && out.is_contiguous(),
                           "out: expected q's shape, type and device, contiguous");
@@ -357,6 +373,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float* lse = nullptr;
     if (a[10] != Py_None) {
         const at::Tensor& l = tensor(a[10], "lse");
+        no_grad(l, "lse", "attention over the cache");
         TORCH_CHECK_VALUE(l.dim() == 2 && l.size(0) == total && l.size(1) == heads_q &&
                               l.scalar_type() == at::kFloat && l.device() == c->device &&
                               l.is_contiguous(),

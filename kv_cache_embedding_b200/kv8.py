@@ -52,12 +52,13 @@ class Rope:
 
     def apply(self, x, pos, out=None, transpose=False):
         """x [T, heads, d] turned to positions pos [T] int64 (transpose: by the
-        transposed matrix, the gradient).  out may be x (contiguous heads)."""
-        return N.rope(self._h, x, pos, out, transpose)
+        transposed matrix), with a gradient.  Into out, which may be x (contiguous
+        heads), without one: tensors that require it are refused."""
+        y = N.rope(self._h, x, pos, out, transpose)
+        return _RopeFn.apply(x, pos, self, bool(transpose)) if y is None else y
 
     def __call__(self, x, pos):
-        """apply(x, pos) with a gradient."""
-        return _RopeFn.apply(x, pos, self, False)
+        return self.apply(x, pos)
 
 
 class KV8Cache:
@@ -147,7 +148,8 @@ class KV8Cache:
 
     def append(self, layer, k, v, cu, max_new, slots=None, rope=None):
         """Writes k, v [total, heads, d] as the last cu[i+1] - cu[i] (at most
-        max_new) tokens of every slot; rope turns the keys to their positions."""
+        max_new) tokens of every slot; rope turns the keys to their positions.  No
+        gradient: tensors that require one are refused (attention's too)."""
         N.append(self._h, layer, k, v, cu, max_new, slots, None if rope is None else rope._h)
 
     def read(self, layer, begin, cu, total, max_count, slots=None, dtype=torch.bfloat16):
