@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/InferenceMode.h>
@@ -85,6 +86,19 @@ bool wants_grad(const at::Tensor& x) { return backward_grad(x) || x._fw_grad(0).
 void no_grad(const at::Tensor& x, const char* name, const char* call) {
     TORCH_CHECK_VALUE(!wants_grad(x), name, ": ", call, " has no gradient; detach() the tensor, or call it under "
                       "torch.no_grad()");
+}
+
+// A tensor that a call has written into: a graph that holds its old values is to know.
+void written(const at::Tensor& x) {
+    if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+}
+// An output whose elements share no memory with each other, and with the input's either
+// none or that of the same element.
+void disjoint(const at::Tensor& out, const at::Tensor& in) {
+    TORCH_CHECK_VALUE(at::has_internal_overlap(out) != at::MemOverlap::Yes,
+                      "out: expected a tensor whose elements lie apart");
+    TORCH_CHECK_VALUE(at::get_overlap_status(out, in) != at::MemOverlapStatus::Partial,
+                      "out: overlaps the input in part");
 }
 
 // A contiguous [n] index tensor.
@@ -210,12 +224,14 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(out.sizes() == x.sizes() && out.scalar_type() == x.scalar_type() &&
                               out.device() == x.device() && out.stride(2) == 1,
                           "out: expected x's shape, type and device, contiguous heads");
+        disjoint(out, x);
     }
     TORCH_CHECK_VALUE(heads <= INT32_MAX, "x: too many heads");
     check("tq_rope", tq_rope(r, T, (int)heads, x.data_ptr(), x.stride(0), x.stride(1),
                              code_of(x.scalar_type()), pos, out.data_ptr(), out.stride(0),
                              out.stride(1), PyObject_IsTrue(a[4]),
                              c10::cuda::getCurrentCUDAStream(x.device().index()).stream()));
+    if (a[3] != Py_None) written(out);
     return THPVariable_Wrap(std::move(out));
     TQ_PY_END
 }
@@ -369,10 +385,12 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(out.sizes() == q.sizes() && out.scalar_type() == q.scalar_type() &&
                               out.device() == c->device && out.is_contiguous(),
                           "out: expected q's shape, type and device, contiguous");
+        disjoint(out, q);
     }
     float* lse = nullptr;
+    at::Tensor l;
     if (a[10] != Py_None) {
-        const at::Tensor& l = tensor(a[10], "lse");
+        l = tensor(a[10], "lse");
         no_grad(l, "lse", "attention over the cache");
         TORCH_CHECK_VALUE(l.dim() == 2 && l.size(0) == total && l.size(1) == heads_q &&
                               l.scalar_type() == at::kFloat && l.device() == c->device &&
@@ -402,6 +420,8 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 q.data_ptr(), code_of(q.scalar_type()), q.stride(0), q.stride(1),
                                 (float)scale, causal, window, out.data_ptr(), fresh, lse, w.ptr,
                                 w.bytes, s));
+    if (!fresh) written(out);
+    if (lse) written(l);
     return THPVariable_Wrap(std::move(out));
     TQ_PY_END
 }

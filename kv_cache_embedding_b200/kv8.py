@@ -163,7 +163,8 @@ class KV8Cache:
         """Attention of q [total, heads_q, d] (bfloat16 or float16), the last
         cu[i+1] - cu[i] (at most max_q) tokens of every slot, over the slot's
         tokens: [total, heads_q, d].  Rows of q behind cu[-1] are 0 in the result, or
-        stay as they were in an `out` (contiguous) that is given.  scale defaults to 1/sqrt(d); window > 0: a
+        stay as they were in an `out` (contiguous, q's own memory or none of it) that is
+        given.  scale defaults to 1/sqrt(d); window > 0: a
         token sees the last `window` keys, itself included; lse: [total, heads_q]
         float32, filled where given."""
         return N.attention(self._h, layer, q, cu, max_q, slots, scale, causal, window, out, lse)

@@ -65,3 +65,46 @@ def test_the_cache_refuses_gradients(tq_lib, cuda):
         with pytest.raises(ValueError):
             c.attention(0, fwAD.make_dual(q, torch.ones_like(q)), cu, 1)
     c.status()
+
+
+def test_outputs_that_a_graph_holds(tq_lib, cuda):
+    """A tensor that is written into counts as changed: a backward pass that needs
+    its old values says so."""
+    r = tq_lib.Rope(64)
+    c = fill(tq_lib, cuda, "i8", 2, 64, 32, [40])
+    pos, cu = torch.arange(1, device=cuda), cu_of([1], cuda)
+    q = torch.randn(1, 4, 64, device=cuda).to(torch.bfloat16)
+
+    def held(shape, dtype, write):
+        t = torch.randn(shape, device=cuda).to(dtype)
+        w = torch.ones_like(t).requires_grad_()
+        y = (w * t).sum()
+        write(t)
+        with pytest.raises(RuntimeError):
+            y.backward()
+    held((1, 4, 64), torch.bfloat16, lambda t: r.apply(t, pos, out=t))
+    held((1, 4, 64), torch.bfloat16, lambda t: c.attention(0, q, cu, 1, out=t))
+    held((1, 4), torch.float32, lambda t: c.attention(0, q, cu, 1, lse=t))
+    with torch.inference_mode():
+        t = torch.randn(1, 4, 64, device=cuda)
+        r.apply(t, pos, out=t)
+    r.apply(t, pos, out=t)  # (a tensor without a version)
+
+
+def test_outputs_that_overlap(tq_lib, cuda):
+    r = tq_lib.Rope(64)
+    c = fill(tq_lib, cuda, "i8", 2, 64, 32, [40])
+    pos = torch.arange(3, device=cuda)
+    x = torch.randn(3, 4, 64, device=cuda)
+    line = torch.randn(4 * 4 * 64, device=cuda)
+    with pytest.raises(ValueError):  # one row for all tokens
+        r.apply(x, pos, out=torch.empty(1, 4, 64, device=cuda).expand(3, 4, 64))
+    with pytest.raises(ValueError):  # shifted by a token
+        r.apply(line[:768].view(3, 4, 64), pos, out=line[256:].view(3, 4, 64))
+    half = line.to(torch.bfloat16)
+    with pytest.raises(ValueError):
+        c.attention(0, half[:768].view(3, 4, 64), cu_of([3], cuda), 3, out=half[256:].view(3, 4, 64))
+    r.apply(x, pos, out=x)
+    whole = half[:768].view(3, 4, 64)
+    want = c.attention(0, whole, cu_of([3], cuda), 3)  # the same memory: each row after it is read
+    assert torch.equal(c.attention(0, whole, cu_of([3], cuda), 3, out=whole), want)
