@@ -25,13 +25,32 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale():
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+def _older(path, deps):
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
+
+
+def _stale_lib():
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return _older(LIB, deps + [os.path.join(INCLUDE, "tq.h")])
+
+
+def _torch_version():
+    from importlib.metadata import version
+    return version("torch")
+
+
+def _stale_bind():
+    """_kv8.so is older than its sources, or built for another torch (whose C++
+    interface it is bound to)."""
+    deps = [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "tq.h")]
+    if _older(BIND, deps):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    deps = [BIND_SRC] + sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-    deps.append(os.path.join(INCLUDE, "tq.h"))
-    return any(os.path.getmtime(p) > t for p in deps)
+    with open(BIND, "rb") as f:
+        return b"built for torch " + _torch_version().encode() + b"\0" not in f.read()
+
+
+def _stale():
+    return _stale_lib() or _stale_bind()
 
 
 def _bind_command(out):
@@ -46,6 +65,7 @@ def _bind_command(out):
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return ["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-DTQ_TORCH={_torch_version()}",
             *(f"-I{i}" for i in inc), BIND_SRC, "-o", out,
             f"-L{PKG}", "-l:libtq.so", "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(root, 'lib')}",
             "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
@@ -53,9 +73,17 @@ def _bind_command(out):
 
 def build(force=False, verbose=False):
     """Compile every .cu under csrc/ for sm_100a and link libtq.so (static
-    CUDA runtime; the driver API is reached through cudaGetDriverEntryPoint)."""
-    if not force and not _stale():
-        return LIB
+    CUDA runtime; the driver API is reached through cudaGetDriverEntryPoint);
+    then _kv8.so."""
+    if force or _stale_lib():
+        _build_lib(verbose)
+    if force or _stale_bind():
+        subprocess.check_call(_bind_command(BIND + ".tmp"))
+        os.replace(BIND + ".tmp", BIND)
+    return LIB
+
+
+def _build_lib(verbose):
     nvcc = os.environ.get("NVCC", "nvcc")
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -75,9 +103,6 @@ def build(force=False, verbose=False):
     cmd = [nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp, *objs]
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
-    subprocess.check_call(_bind_command(BIND + ".tmp"))
-    os.replace(BIND + ".tmp", BIND)
-    return LIB
 
 
 if __name__ == "__main__":

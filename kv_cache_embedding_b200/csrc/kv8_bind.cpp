@@ -450,4 +450,16 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_kv8", nullptr, -1, g_methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kv8() { return PyModule_Create(&g_module); }
+// The torch that the module is built for (build.py looks for it in the file).
+#define TQ_STR2(x) #x
+#define TQ_STR(x) TQ_STR2(x)
+static const char kTorch[] = "built for torch " TQ_STR(TQ_TORCH);
+
+PyMODINIT_FUNC PyInit__kv8() {
+    PyObject* m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "built_for", kTorch) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -8,9 +8,27 @@ import ctypes
 import torch
 
 from . import _binding as B
-from . import _kv8 as N  # built beside libtq.so (build.py)
 
-N.init(B.TQError)
+N = None  # the native module
+
+
+def _native():
+    """Loads _kv8.so, built beside libtq.so for one version of torch; the rest of
+    the package does without it."""
+    global N
+    if N is None:
+        hint = "run `python kv_cache_embedding_b200/build.py`"
+        try:
+            from . import _kv8 as module
+        except ImportError as e:
+            raise ImportError(f"_kv8.so does not load ({e}); {hint}") from e
+        if module.built_for != f"built for torch {torch.__version__}":
+            raise ImportError(f"_kv8.so is {module.built_for}, this is {torch.__version__}; {hint}")
+        module.init(B.TQError)
+        N = module
+    return N
+
+
 _FORMATS = {torch.int8: B.TQ_KV_I8, torch.float8_e4m3fn: B.TQ_KV_E4M3}
 _LAYOUTS = {"half": B.TQ_ROPE_HALF, "interleaved": B.TQ_ROPE_INTERLEAVED}
 _SCALINGS = {"none": B.TQ_ROPE_PLAIN, "linear": B.TQ_ROPE_LINEAR, "ntk": B.TQ_ROPE_NTK,
@@ -48,7 +66,7 @@ class Rope:
         B.tq_build_rope(self.d, self.rot, float(base), _LAYOUTS[layout], _SCALINGS[scaling],
                         float(factor), float(ctx), float(low), float(high), float(amplitude),
                         self.params)
-        self._h = N.rope_params(ctypes.addressof(self.params))
+        self._h = _native().rope_params(ctypes.addressof(self.params))
 
     def apply(self, x, pos, out=None, transpose=False):
         """x [T, heads, d] turned to positions pos [T] int64 (transpose: by the
@@ -101,7 +119,7 @@ class KV8Cache:
                             vscale.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),
                             self._status.data_ptr())
         # the workspaces live there, one a stream
-        self._h = N.cache(ctypes.addressof(self.c), self._status)
+        self._h = _native().cache(ctypes.addressof(self.c), self._status)
 
     @classmethod
     def empty(cls, layers, pages, heads, d, slots, max_pages, page=64, dtype=torch.int8,

@@ -1,0 +1,60 @@
+"""The package around the 8-bit cache's native module, without a GPU."""
+import importlib.util
+import os
+import subprocess
+import sys
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PKG = os.path.join(ROOT, "kv_cache_embedding_b200")
+
+
+def copy_of_the_package(tmp_path, leave_out):
+    """Links to the package's files but one."""
+    pkg = tmp_path / "kv_cache_embedding_b200"
+    pkg.mkdir()
+    for name in os.listdir(PKG):
+        if name.endswith((".py", ".so")) and name != leave_out:
+            os.symlink(os.path.join(PKG, name), pkg / name)
+    return pkg
+
+
+def run(tmp_path, code):
+    p = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
+
+
+def test_the_package_needs_the_native_module_for_the_8_bit_cache_alone(tq_lib, tmp_path):
+    copy_of_the_package(tmp_path, "_kv8.so")
+    run(tmp_path, """
+import kv_cache_embedding_b200 as tq
+assert tq.TurboQuant and tq.tq_encode and tq.KV8Cache
+for make in (lambda: tq.Rope(64), lambda: tq.KV8Cache.empty(1, 1, 1, 64, 1, 1, device="cpu")):
+    try:
+        make()
+    except ImportError as e:
+        assert "build.py" in str(e)
+    else:
+        raise SystemExit("no error")
+""")
+
+
+def test_a_native_module_of_another_torch(tq_lib, tmp_path):
+    """Refused by name when it is used, and built again."""
+    copy_of_the_package(tmp_path, None)
+    run(tmp_path, """
+import torch
+torch.__version__ = "0.0.1"
+import kv_cache_embedding_b200 as tq
+try:
+    tq.Rope(64)
+except ImportError as e:
+    assert "0.0.1" in str(e) and "build.py" in str(e)
+else:
+    raise SystemExit("no error")
+""")
+    spec = importlib.util.spec_from_file_location("_tq_build_again", os.path.join(PKG, "build.py"))
+    kb = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(kb)
+    assert not kb._stale()
+    kb._torch_version = lambda: "0.0.1"
+    assert kb._stale()
