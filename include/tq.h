@@ -369,9 +369,9 @@ TQ_API int tq_topk_noalloc(const tq_codebook_t *cb, const float *d_Pi, const flo
                              f_i (g_i + (1 - g_i)/factor)                             */
 
 /* Rotation parameters (host, plain data, filled by tq_build_rope, passed by
- * value to the kernels).  turns[i] = f_i / 2 pi in turns, as a fraction of 2^64:
- * position times turns[i], modulo 2^64, is the exact fraction of a turn, so an
- * angle keeps its precision at every 64-bit position (no tables). */
+ * value to the kernels).  turns[i] = f_i / 2 pi in turns, as a fraction of 2^64 and
+ * within two units of it: position times turns[i], modulo 2^64, is the fraction of a
+ * turn, off by |position| 2^-63 turn at most (2^-23 at position 2^40; no tables). */
 typedef struct tq_rope_params {
     int32_t  d;          /* head dimension, even, 2..256                      */
     int32_t  rot;        /* rotated coordinates (the first ones), even, 0..d  */
@@ -380,7 +380,7 @@ typedef struct tq_rope_params {
     uint64_t turns[128];
 } tq_rope_params_t;
 
-/* Fills *r (host only, fp64).  scaling: a rule above; factor >= 1 (ignored by
+/* Fills *r (host only, in long double).  scaling: a rule above; factor >= 1 (ignored by
  * PLAIN); ctx, low, high: PARTS only (ctx > 0, low < high).  base > 1.
  * TQ_ERR_ARG for a bad enum or a non-finite or out-of-range number,
  * TQ_ERR_UNSUPPORTED for d or rot outside the ranges above. */

@@ -164,24 +164,26 @@ extern "C" int tq_build_rope(int d, int rot, double base, int layout, int scalin
     if (scaling == TQ_ROPE_PARTS && (!std::isfinite(ctx) || ctx <= 0.0 || !std::isfinite(low) ||
                                      !std::isfinite(high) || low >= high))
         return TQ_ERR_ARG;
-    const double two_pi = 6.283185307179586476925;
+    // (long double: 64 bits of mantissa, for positions far out)
+    const long double two_pi = 6.283185307179586476925286766559L;
     tq_rope_params_t p = {};
     p.d = d;
     p.rot = rot;
     p.layout = layout;
     p.amplitude = (float)amplitude;
-    if (scaling == TQ_ROPE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
-    if (!std::isfinite(base)) return TQ_ERR_ARG;
+    long double b = base;
+    if (scaling == TQ_ROPE_NTK) b *= std::pow((long double)factor, (long double)rot / (rot - 2));
+    if (b > 1.7976931348623157e308L) return TQ_ERR_ARG;
     for (int i = 0; i < rot / 2; ++i) {
-        double f = std::pow(base, -2.0 * i / rot);
+        long double f = std::pow(b, -2.0L * i / rot);
         if (scaling == TQ_ROPE_LINEAR) f /= factor;
         if (scaling == TQ_ROPE_PARTS) {
-            double g = (ctx * f / two_pi - low) / (high - low);
-            g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
-            f *= g + (1.0 - g) / factor;
+            long double g = (ctx * f / two_pi - low) / ((long double)high - low);
+            g = g < 0.0L ? 0.0L : (g > 1.0L ? 1.0L : g);
+            f *= g + (1.0L - g) / factor;
         }
-        // 0 < f <= 1 radian: below 1/6 turn; 2^64 times it keeps fp64's precision
-        p.turns[i] = (uint64_t)std::llrint(std::ldexp(f / two_pi, 63)) << 1;
+        // 0 < f <= 1 radian: below 1/6 turn
+        p.turns[i] = (uint64_t)std::llrint(std::ldexp(f / two_pi, 64));
     }
     *r = p;
     return TQ_OK;

@@ -8,8 +8,8 @@
 namespace tq {
 
 // cos and sin of a position's angle.  `turns` is the frequency in turns as a
-// fraction of 2^64, so pos * turns modulo 2^64 is the fraction of a turn exactly
-// (two's complement takes negative positions along); its top 32 bits leave an
+// fraction of 2^64, so pos * turns modulo 2^64 is that frequency's fraction of a turn
+// exactly (two's complement takes negative positions along); its top 32 bits leave an
 // error of 2^-32 turn.  The nearest quarter turn is taken off in integers: what
 // is left, within 1/8 turn, rounds to fp32 with an error below 2^-24 of itself.
 __device__ __forceinline__ void rope_angle(uint64_t turns, int64_t pos, float& c, float& s) {

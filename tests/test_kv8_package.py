@@ -1,8 +1,11 @@
 """The package around the 8-bit cache's native module, without a GPU."""
+import decimal
 import importlib.util
 import os
 import subprocess
 import sys
+
+import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PKG = os.path.join(ROOT, "kv_cache_embedding_b200")
@@ -58,3 +61,26 @@ else:
     assert not kb._stale()
     kb._torch_version = lambda: "0.0.1"
     assert kb._stale()
+
+
+@pytest.mark.parametrize("scaling", ["none", "linear", "ntk", "parts"])
+@pytest.mark.parametrize("d,rot,base", [(128, 128, 1e4), (128, 64, 5e5), (256, 256, 1e6), (8, 6, 3.0)])
+def test_rope_frequencies_of_far_positions(tq_lib, scaling, d, rot, base):
+    """turns[i] against f / 2 pi in 60 digits.  The host computes it with 64 bits of
+    mantissa: a handful of roundings (pow within a unit, the rule's products, the
+    division by 2 pi, the rounding to the fraction) of 2^-64 of at most 0.16 turn and
+    half a unit of 2^-64: 2 units, so an angle at position p is within |p| 2^-63 turn."""
+    r = tq_lib.Rope(d, rot, base=base, scaling=scaling, factor=4.0, ctx=4096, low=1.0, high=32.0)
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        D = decimal.Decimal
+        pi = D("3.14159265358979323846264338327950288419716939937510582097494")
+        b = D(base) * D(4) ** (D(rot) / D(rot - 2)) if scaling == "ntk" else D(base)
+        for i in range(rot // 2):
+            f = (b.ln() * D(-2 * i) / D(rot)).exp()
+            if scaling == "linear":
+                f /= 4
+            if scaling == "parts":
+                g = min(D(1), max(D(0), (D(4096) * f / (2 * pi) - 1) / 31))
+                f = f * g + f / 4 * (1 - g)
+            assert abs(D(r.params.turns[i]) - f / (2 * pi) * 2 ** 64) <= 2, i
