@@ -6,10 +6,10 @@
 // of halves (row_unit), so <q, c> is a sum of exact products in fp32.  The
 // block scales never touch the codes: s_k multiplies the logit, s_v the
 // probability, and the product is rounded to a half (2^-11) in units of its own
-// row's: with m the row's largest logit so far and q that of l + log2 s_v, rounded
-// down, it is multiplied by 2^(m - q + 14), which puts the row's largest product
-// between 2^13 and 2^15; what is smaller than halves' normal range is off by 2^-38 of
-// that largest one.  Keys that the row does not see have no part in the unit.
+// row's, a power of two by which the row's largest product so far is at 2^10 at least:
+// what is smaller than halves' normal range is off by 2^-35 of that largest one, and
+// keys that the row does not see have no part in it.  (The unit is kept relative to the
+// reference of the logits, which may be so large that their last bits are whole units.)
 // Maximum, sum and output are fp32.
 //
 // Work.  Reading the cache is the cost (2 d bytes a token and KV head for up to
@@ -76,6 +76,7 @@ constexpr int kRows = 16;     // query rows of an item, at most
 constexpr int kWarps = 12;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kItemTiles = 4 * kWarps;  // see "sharing out"
+constexpr float kStart = 11.f;  // a row's largest product: at 2^(kStart - 1) at least
 template <int D>
 constexpr int kStages = D == 128 ? 2 : 4;  // 16 KB of a warp's ring
 
@@ -502,7 +503,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
         // the query rows as MMA columns: this thread loads row 8 nb + r0, and keeps
         // the sums of rows 8 nb + 2 c2 + {0, 1}: column 2 nb + {0, 1}
         uint32_t qf[NB][CH][2];
-        float sl[2 * NB], m[2 * NB], q2[2 * NB], L[2 * NB];  // q2: of l + log2 s_v
+        float sl[2 * NB], m[2 * NB], up[2 * NB], L[2 * NB];  // o in units of 2^(m - up), L of 2^m
         int lim[2 * NB], low[2 * NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -531,12 +532,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                 sl[u] = a.scale_log2 / __shfl_sync(0xffffffffu, unit_q, 4 * (2 * c2 + j));
                 lim[u] = a.causal ? min(pos, e.len - 1) : e.len - 1;
                 low[u] = below_window(a, pos);
-                m[u] = q2[u] = -INFINITY;
+                m[u] = kNoKey;
+                up[u] = 0.f;
                 L[u] = 0.f;
             }
         }
-        // A column's sums o are in units of 2^-unit (a row of zero scales: any unit)
-        auto unit_of = [](float m, float q) { return (int)floorf(fminf(m - q, 106.f)) + 14; };
         // keys below `clear` and above `low_any` need no mask for any row
         const int clear = a.causal ? min(e.len - e.qn, e.len - 1) : e.len - 1;
         const int low_any = below_window(a, e.len - 1);
@@ -605,38 +605,35 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                         mx[b][k & 1] = fmaxf(mx[b][k & 1], l);
                     }
                 }
-                float base[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int u = 2 * nb + j;
-                    float top = fmaxf(mx[0][j], mx[1][j]), topq = fmaxf(mx[0][j] + es[0], mx[1][j] + es[1]);
+                    float top = fmaxf(mx[0][j], mx[1][j]);
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    if (es[0] == es[1]) {  // (all tiles where a page holds them whole)
-                        topq = top + es[0];
-                    } else {
-#pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) topq = fmaxf(topq, __shfl_xor_sync(0xffffffffu, topq, x));
-                    }
                     const float m0 = m[u];
-                    const int unit0 = unit_of(m0, q2[u]);
-                    m[u] = fmaxf(m0, top);
-                    q2[u] = fmaxf(q2[u], topq);
-                    const int unit = unit_of(m[u], q2[u]);
-                    base[j] = m[u] == -INFINITY ? 0.f : m[u];
-                    L[u] *= ex2(m0 - base[j]);
-                    alpha[u] = ex2(m0 - base[j] + (float)(unit - unit0));
+                    if (top - m0 > kGrow) m[u] = ceilf(top);
+                    float topv = top - m[u] + es[0];
+                    if (es[0] != es[1]) {  // (the same in all tiles that one page holds)
+                        topv = fmaxf(mx[0][j] - m[u] + es[0], mx[1][j] - m[u] + es[1]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, x));
+                    }
+                    const float follow = up[u] + (m[u] - m0);
+                    up[u] = new_up(follow, topv, kStart);
+                    alpha[u] = ex2(up[u] - follow);
                     rescale |= alpha[u] != 1.f;
+                    L[u] *= ex2(m0 - m[u]);
                     // (a hidden page's may be anything: it meets zeros)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) w[b][j] = fminf(vs[b] * pow2(unit), kLargestFloat);
+                    for (int b = 0; b < 2; ++b) w[b][j] = fminf(vs[b] * pow2(up[u]), kLargestFloat);
                 }
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     float pr[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        pr[k] = ex2(s[nb][b][k] - base[k & 1]);
+                        pr[k] = ex2(s[nb][b][k] - m[2 * nb + (k & 1)]);
                         L[2 * nb + (k & 1)] += pr[k];
                     }
                     // keys x columns, transposed into the B operand
@@ -699,7 +696,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             for (int x = 4; x < 32; x <<= 1) L[u] += __shfl_xor_sync(0xffffffffu, L[u], x);
             const int r = 8 * (u >> 1) + 2 * c2 + (u & 1), j = u & 1, nb = u >> 1;
             if (r >= nrows) continue;
-            const float size = pow2(-unit_of(m[u], q2[u]));
+            const float size = pow2(-up[u]);
             if (begins && ends) {
                 const int64_t tok = e.c0 + r / a.group;
                 const int hq = p.head * a.group + r % a.group;

@@ -116,12 +116,25 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // The exponent e of a value scale, 2^e <= s < 2^(e + 1) (below fp32's normal range
-// -127, an upper bound still); -infinity for 0.  2^e for -126 <= e <= 127.
+// -127, an upper bound still); -infinity for 0.  2^e of a whole number from -126 to 127:
+// behind 1.5 2^23 the last bits of a sum are the integer.
 __device__ __forceinline__ float scale_exp(float s) {
     return s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : -INFINITY;
 }
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ float pow2(float e) { return __uint_as_float(__float_as_uint(e + 12583039.f) << 23); }
 constexpr float kLargestFloat = 3.40282347e38f;
+
+// Units of a row: probabilities are 2^(l - m), their products with the value scales are
+// summed as P s_v 2^up.  m and up are whole numbers that follow when a probability
+// passes 2^kGrow or a product 2^kRoom (a half ends at 2^16).  Before a row's first key m
+// is kNoKey: what there is of sums is multiplied by 0 then.
+constexpr float kGrow = 8.f, kRoom = 14.f, kNoKey = -1e38f;
+// From up, the change of m and the largest log2 (P s_v) + m - m_new among new keys (off
+// by up to one), the new up; start: where the largest product is put.  (A row whose
+// values are far below its probabilities: as far as fp32 goes.)
+__device__ __forceinline__ float new_up(float follow, float top, float start) {
+    return fminf(top + follow > kRoom ? start - ceilf(top) : follow, 120.f);
+}
 
 // The power of two that brings a row's largest magnitude into [2^15, 2^16), the top
 // of a half's range: with it a row of bf16 is a row of halves, exact down to 2^-32 of

@@ -1,14 +1,14 @@
 // Attention over the 8-bit paged cache, many query rows (prompts, chunks behind
 // a prefix, drafts): the sums of tq_kv8_attention.cu on the sm_100a tensor cores.
 //
-//   S = Q C_k^T   (rows x 128 keys),   P = 2^(S s_k s_q - m),   O += (P s_v 2^(m - r)) C_v
+//   S = Q C_k^T   (rows x 128 keys),   P = 2^(S s_k s_q - m),   O += (P s_v 2^u) C_v
 //
 // with the codes C as exact halves, Q a row of halves times a power of two, s_k
-// and s_v one number per 16 keys (a page at least).  m and r are the row's own: whole
-// numbers near the largest logit and the largest log2 (P s_v) + m of the keys that it
-// sees, so that P s_v 2^(m - r) is rounded to a half (2^-11) with the largest one at
-// 2^5 at least: what is smaller than halves' normal range is off by 2^-30 of that one,
-// and no page that the row does not see has a part in it.  Sums are fp32.
+// and s_v one number per 16 keys (a page at least).  m and u are the row's own: whole
+// numbers by which the largest P of the keys that it sees is near 1, and the largest
+// P s_v 2^u, which is rounded to a half (2^-11), at 2^5 at least: what is smaller than
+// halves' normal range is off by 2^-30 of that one, and no page that the row does not
+// see has a part in it.  Sums are fp32.
 //
 // A CTA runs items of 256 rows (two stages of 128) of one entry and KV head over
 // tiles of 128 keys; the steps (item x tile) of the whole batch are shared out
@@ -17,9 +17,9 @@
 // joined by k_prompt_merge.  Warps:
 //   0-3, 4-7  softmax of stage 0, 1: a thread a row, half a tile (64 keys) at a time.
 //             Loads its query row, turns S (tensor memory) into P in place, rescales
-//             O only when the row's largest product has grown by more than 2^8 (the
-//             reference r then follows; the product is below 2^15 meanwhile, inside a
-//             half's range), writes the result.
+//             O only when the row's largest product has grown by more than 2^8 (u then
+//             follows; the product is below 2^15 meanwhile, inside a half's range),
+//             writes the result.
 //   8-11      codes -> halves: from the TMA ring (128 keys x d bytes) into the
 //             swizzled operand tiles of K (K-major) and V (the same rows, read
 //             MN-major), with the tile's scales.
@@ -57,9 +57,7 @@ constexpr int kGroups = kPT / 16;   // scale groups of a tile
 constexpr int kRing = 4;            // tiles whose scales are kept
 constexpr int kWorks = 4;           // items that are handed out ahead
 constexpr uint32_t kTmemCols = 512;
-constexpr float kGrow = 8.f;        // log2 of how far a probability may pass 1
-constexpr float kRoom = 14.f;       // P stays below 2^(kRoom + 1), a half's range,
-constexpr float kStart = 6.f;       // and is put between 2^(kStart - 1) and 2^(kStart + 1)
+constexpr float kStart = 6.f;       // a row's largest product: at 2^(kStart - 1) at least
 
 // A CTA's piece of an item, as the warps get it.
 struct Work {
@@ -320,9 +318,8 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
             const int pos = w.pos0 + tq, len = w.len;
             const int lim = valid && a.causal ? min(pos, len - 1) : len - 1;
             const int low = valid ? below_window(a, pos) : -1;
-            // the references, whole numbers once there is a key: L is in units of 2^m,
-            // O of 2^r, lift is 2^(m - r)
-            float m = -INFINITY, r = -INFINITY, lift = 1.f;
+            // L is in units of 2^m, O of 2^(m - up), lift is 2^up
+            float m = kNoKey, up = 0.f, lift = 1.f;
             float2 L2 = make_float2(0.f, 0.f);
             const uint32_t first = halves, last = halves + 2 * (t_end - t_begin);
             for (int key0 = (w.t0 + t_begin) * kPT; halves < last; key0 += kPH) {
@@ -342,7 +339,17 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     tg[g] = -INFINITY;
                 }
                 const uint32_t absent = sm.absent[rg] >> 4 * h & 15u;
-                const bool masked = __any_sync(0xffffffffu, key0 + kPH - 1 > lim || key0 <= low || absent);
+                // a half tile that a mask touches, or with rows of logits beyond 2^22 (an
+                // item's first: that could be; rows that are not finite aside): there logits
+                // are rounded before m is taken off.  What the fused product of the other
+                // way keeps of such would be whole units
+                const float size_m = fabsf(m);
+                bool far = size_m > 4194304.f && size_m < -kNoKey;
+                if (halves == first) {
+                    const float most = fmaxf(max3(cg[0], cg[1], cg[2]), cg[3]);
+                    far = most > 4194304.f / (65536.f * code_max<FMT>() * D) && most < 1e25f;
+                }
+                const bool masked = __any_sync(0xffffffffu, key0 + kPH - 1 > lim || key0 <= low || absent || far);
                 // 32 keys are on their way while the 32 before them are looked at
                 if (masked) {
 #pragma unroll
@@ -371,20 +378,25 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     }
                 }
                 const float* ve = &sm.vexp[rg][4 * h];
+                // log2 of the largest P and P s_v, relative to m: logits may be so large
+                // that their own last bits are whole units
                 const float top = fmaxf(max3(tg[0], tg[1], tg[2]), tg[3]);
-                const float topr = fmaxf(max3(tg[0] + ve[0], tg[1] + ve[1], tg[2] + ve[2]), tg[3] + ve[3]);
+                auto largest = [&] {
+                    return fmaxf(max3(tg[0] - m + ve[0], tg[1] - m + ve[1], tg[2] - m + ve[2]), tg[3] - m + ve[3]);
+                };
+                float topv = largest();
                 // the references follow when what they are of has grown out of their range
                 float shrink = 1.f;
-                if (top > m + kGrow || topr > r + kRoom) {
-                    const float m0 = m, r0 = r;
+                if ((top - m > kGrow) | (topv + up > kRoom)) {
+                    const float m0 = m;
                     m = fmaxf(m, ceilf(top));
-                    // (far below the probabilities: out of fp32's range)
-                    r = max3(r, ceilf(topr) - kStart, m - 120.f);
-                    lift = ex2(m - r);
-                    const float f = ex2(m0 - m);  // 0 from -infinity
+                    topv = largest();
+                    const float f = ex2(m0 - m), follow = up + (m - m0);
                     L2.x *= f;
                     L2.y *= f;
-                    shrink = ex2(r0 - r);
+                    up = new_up(follow, topv, kStart);
+                    lift = pow2(up);
+                    shrink = ex2(up - follow);
                 }
                 if (halves > first && __any_sync(0xffffffffu, shrink != 1.f)) {
                     // O holds all halves before this one when the last one's MMAs are done
@@ -403,7 +415,7 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         tmem_st16(o_col + c, o);
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : -m;
+                const float base = -m;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t p[16];

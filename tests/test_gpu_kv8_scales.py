@@ -149,3 +149,28 @@ def test_small_query_coordinates(tq_lib, cuda, count):
     q[..., 64:] *= 2.0 ** -20
     q[..., :64] = 1.0
     check(c, "i8", q.to(torch.bfloat16).to(cuda), [count], [n], scale=2.0 ** 20)
+
+
+@pytest.mark.parametrize("count", [1, 3, 40])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("top", [1e3, 3e7, 1e9, 1e12, -1e9, 1e30])
+def test_large_logits(tq_lib, cuda, count, page, top):
+    """One key's logit is twice as large as any other's, up to 1e30: the result is its
+    value, to the rounding of a probability of 1 times a scale (2^-11) and the type's."""
+    n = 300
+    c = fill(tq_lib, cuda, "i8", 1, 128, page, [n], scale_range=(0.9, 1.1))
+    sign = 1 if top > 0 else -1
+    c.k.copy_(c.k.abs().clamp(1, 50) * sign)
+    c.kscale.fill_(0.01)
+    at = int(c.table[0, 70 // page]), 70 % page
+    c.k[0, at[0], 0, at[1]] = 100 * sign
+    q = torch.ones(count, 2, 128, dtype=torch.bfloat16, device=cuda)
+    lse = torch.zeros(count, 2, device=cuda)
+    out = c.attention(0, q, cu_of([count], cuda), count, scale=top / 128, lse=lse)
+    c.status()
+    want = values(c, "v", 0, 0, n)[0, 70]
+    if top < 0:  # (the sign of the codes and of the scale: the logits are positive)
+        assert (lse > 0).all()
+    far = (out.cpu().double() - want).abs()
+    assert (far <= want.abs() * (2.0 ** -11 + U[torch.bfloat16]) * (1 + 2.0 ** -8) + 1e-12).all()
+    assert ((lse.cpu().double() / abs(top) - 1).abs() <= 2.0 ** -18).all()
