@@ -96,11 +96,12 @@ __global__ __launch_bounds__(VEC == 8 ? 1024 : 256) void k_append(
     const int slot = slot_of(v, a.slots, seq);
     const int64_t c0 = max(a.cu[seq], 0);
     const int count = (int)(min((int64_t)a.cu[seq + 1], a.total) - c0);
-    if (slot < 0 || count <= 0) return;
+    if (slot < 0) return;
     if (count > a.max_new || a.cu[seq + 1] > a.total) {  // not what the host launched for
         if (threadIdx.x == 0) leave_status(v, TQ_ERR_ARG);
         return;
     }
+    if (count <= 0) return;
     const int len = length_of(v, slot);
     // tokens before the slot's first position have no place
     const int start = max(len - count, 0), skip = max(count - len, 0);

@@ -49,7 +49,8 @@ def test_attention_counts_beyond_q(tq_lib, cuda, counts):
     assert (out == 0).all()
 
 
-@pytest.mark.parametrize("counts,max_new,short", [([40, 3], 3, 0), ([2, 1], 1, 0), ([3, 5], 5, 1)])
+@pytest.mark.parametrize("counts,max_new,short", [([40, 3], 3, 0), ([2, 1], 1, 0), ([3, 5], 5, 1),
+                                                  ([3, 5], 5, 5), ([3, 5], 5, 7)])
 def test_append_counts_above_max_new(tq_lib, cuda, counts, max_new, short):
     """More tokens than the host said, or than k has: refused, and later calls wait
     for status()."""
