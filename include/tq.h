@@ -514,7 +514,9 @@ TQ_API int tq_kv8_read(const tq_kv8_t *c, int layer, int ns, const int32_t *d_sl
  * (causal only); causal = 0: all keys.  Query head h reads KV head
  * h / (heads_q / heads):
  *   l_j = scale <q, k_j>,  out = sum_j softmax(l)_j v_j,  lse = log sum_j e^l_j;
- * a row that sees no key: out = 0, lse = -infinity.
+ * a row that sees no key: out = 0, lse = -infinity.  (scale: |scale| log2(e) finite in
+ * fp32.  A NaN among the e4m3 codes of a value, which tq_kv8_append never writes, shows
+ * in rows that do not see it.)
  * d_q, d_out: [total_q][heads_q][d] of q_dtype (TQ_BF16 or TQ_F16); q with
  * strides in elements (multiples of 8, the base 16-byte aligned), out
  * contiguous.  d_lse: [total_q][heads_q] fp32 or NULL.  heads_q a multiple of

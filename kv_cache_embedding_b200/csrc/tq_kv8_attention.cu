@@ -844,6 +844,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
 }
 
 constexpr int kMaxBlocks = 148;  // the workspace's size
+constexpr float kLog2e = 1.44269504089f;
 
 // The most steps that a call of these sizes can have (its lengths lie on the
 // device); blocks: one an SM, fewer where the tables are too short to fill them.
@@ -954,7 +955,8 @@ extern "C" int tq_kv8_attention_rows(const tq_kv8_t* c, int layer, int ns, const
     if (layer < 0 || layer >= c->layers || ns < 0 || total_q < 0 || max_q < 0 || heads_q < 1)
         return TQ_ERR_ARG;
     if (q_dtype != TQ_BF16 && q_dtype != TQ_F16) return TQ_ERR_ARG;
-    if (causal < 0 || causal > 1 || window < 0 || (window > 0 && !causal) || !std::isfinite(scale))
+    if (causal < 0 || causal > 1 || window < 0 || (window > 0 && !causal) ||
+        !std::isfinite(scale * kv8::kLog2e))
         return TQ_ERR_ARG;
     if (!d_slots && ns > c->slots) return TQ_ERR_ARG;
     if (heads_q % c->heads || heads_q / c->heads > 128) return TQ_ERR_UNSUPPORTED;
@@ -978,7 +980,7 @@ extern "C" int tq_kv8_attention_rows(const tq_kv8_t* c, int layer, int ns, const
     a.q = d_q;
     a.q_ts = q_ts;
     a.q_hs = q_hs;
-    a.scale_log2 = scale * 1.44269504089f;
+    a.scale_log2 = scale * kv8::kLog2e;
     a.ks = c->d_kscale + layer * kv8::layer_scales(c);
     a.vs = c->d_vscale + layer * kv8::layer_scales(c);
     a.out = d_out;
