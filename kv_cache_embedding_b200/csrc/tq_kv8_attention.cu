@@ -583,16 +583,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             const bool masked = key0 + kTile - 1 > clear || key0 <= low_any || sc.x == -INFINITY ||
                                 sc.y == -INFINITY;
             const float vs[2] = {sc.z, sc.w}, es[2] = {scale_exp(sc.z), scale_exp(sc.w)};
-            uint32_t pf[NB][2][2];
-            float alpha[2 * NB];
-            bool rescale = false;
+            float top[2 * NB];  // the largest logits
+            bool grown = false;
+            const float room = kRoom - fmaxf(es[0], es[1]);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                float mx[2][2], w[2][2];  // [16 keys][column]
+                top[2 * nb] = top[2 * nb + 1] = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const float ks = b == 0 ? sc.x : sc.y;
-                    mx[b][0] = mx[b][1] = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int u = 2 * nb + (k & 1);
@@ -602,34 +601,50 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                             if (key > lim[u] || key <= low[u] || ks == -INFINITY) l = -INFINITY;
                         }
                         s[nb][b][k] = l;
-                        mx[b][k & 1] = fmaxf(mx[b][k & 1], l);
+                        top[u] = fmaxf(top[u], l);
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int u = 2 * nb + j;
-                    float top = fmaxf(mx[0][j], mx[1][j]);
+                for (int u = 2 * nb; u < 2 * nb + 2; ++u) {
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    for (int x = 4; x < 32; x <<= 1) top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], x));
+                    const float d = top[u] - m[u];
+                    grown |= (d > kGrow) | (d + up[u] > room);
+                }
+            }
+            if (__any_sync(0xffffffffu, grown)) {  // units follow, and the sums in them
+#pragma unroll
+                for (int u = 0; u < 2 * NB; ++u) {
                     const float m0 = m[u];
-                    if (top - m0 > kGrow) m[u] = ceilf(top);
-                    float topv = top - m[u] + es[0];
+                    if (top[u] - m0 > kGrow) m[u] = ceilf(top[u]);
+                    float topv = top[u] - m[u] + es[0];
                     if (es[0] != es[1]) {  // (the same in all tiles that one page holds)
-                        topv = fmaxf(mx[0][j] - m[u] + es[0], mx[1][j] - m[u] + es[1]);
+                        topv = -INFINITY;
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            topv = fmaxf(topv, fmaxf(s[u >> 1][b][u & 1], s[u >> 1][b][2 + (u & 1)]) - m[u] + es[b]);
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, x));
                     }
                     const float follow = up[u] + (m[u] - m0);
                     up[u] = new_up(follow, topv, kStart);
-                    alpha[u] = ex2(up[u] - follow);
-                    rescale |= alpha[u] != 1.f;
                     L[u] *= ex2(m0 - m[u]);
-                    // (a hidden page's may be anything: it meets zeros)
+                    const float f = ex2(up[u] - follow);
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) w[b][j] = fminf(vs[b] * pow2(up[u]), kLargestFloat);
+                    for (int i = 0; i < CH; ++i) {
+                        o[u >> 1][i][u & 1] *= f;
+                        o[u >> 1][i][2 + (u & 1)] *= f;
+                    }
                 }
+            }
+            uint32_t pf[NB][2][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float lift[2] = {pow2(up[2 * nb]), pow2(up[2 * nb + 1])};
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
+                    // (a hidden page's scale may be anything: it meets zeros)
+                    const float w[2] = {fminf(vs[b] * lift[0], kLargestFloat), fminf(vs[b] * lift[1], kLargestFloat)};
                     float pr[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -637,17 +652,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                         L[2 * nb + (k & 1)] += pr[k];
                     }
                     // keys x columns, transposed into the B operand
-                    pf[nb][b][0] = movm(pack_half2(pr[0] * w[b][0], pr[1] * w[b][1]));
-                    pf[nb][b][1] = movm(pack_half2(pr[2] * w[b][0], pr[3] * w[b][1]));
+                    pf[nb][b][0] = movm(pack_half2(pr[0] * w[0], pr[1] * w[1]));
+                    pf[nb][b][1] = movm(pack_half2(pr[2] * w[0], pr[3] * w[1]));
                 }
-            }
-            if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int i = 0; i < CH; ++i)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) o[nb][i][k] *= alpha[2 * nb + (k & 1)];
             }
             // e4m3 rows behind the slot's end may hold NaN codes, and 0 NaN is NaN
             if (FMT == TQ_KV_E4M3 && key0 + kTile > e.len) {

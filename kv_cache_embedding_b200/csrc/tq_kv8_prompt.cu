@@ -377,20 +377,18 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                         tg[2 * c + 1] = max16(&s[c][16]) * cg[2 * c + 1];
                     }
                 }
+                // the references follow when what they are of has grown out of their range.
+                // (All relative to m: logits may be so large that their last bits are whole
+                // units.  The first test takes every key for one of the largest scale.)
                 const float* ve = &sm.vexp[rg][4 * h];
-                // log2 of the largest P and P s_v, relative to m: logits may be so large
-                // that their own last bits are whole units
-                const float top = fmaxf(max3(tg[0], tg[1], tg[2]), tg[3]);
-                auto largest = [&] {
-                    return fmaxf(max3(tg[0] - m + ve[0], tg[1] - m + ve[1], tg[2] - m + ve[2]), tg[3] - m + ve[3]);
-                };
-                float topv = largest();
-                // the references follow when what they are of has grown out of their range
+                const float room = kRoom - fmaxf(max3(ve[0], ve[1], ve[2]), ve[3]);
+                const float top = fmaxf(max3(tg[0], tg[1], tg[2]), tg[3]), d = top - m;
                 float shrink = 1.f;
-                if ((top - m > kGrow) | (topv + up > kRoom)) {
+                if ((d > kGrow) | (d + up > room)) {
                     const float m0 = m;
                     m = fmaxf(m, ceilf(top));
-                    topv = largest();
+                    const float topv =
+                        fmaxf(max3(tg[0] - m + ve[0], tg[1] - m + ve[1], tg[2] - m + ve[2]), tg[3] - m + ve[3]);
                     const float f = ex2(m0 - m), follow = up + (m - m0);
                     L2.x *= f;
                     L2.y *= f;
