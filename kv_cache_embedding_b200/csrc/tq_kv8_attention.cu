@@ -283,6 +283,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
     constexpr int CH = D / 16;  // 16-byte chunks of a code row
     constexpr int NS = kStages<D>;
+    // registers are short: a row's limits are formed where a mask is (64 sequences: 104
+    // against 107 us; 16 x 16384 keys 93 against 96; where they are not short it loses)
+    constexpr bool kLean = NB == 1 && D == 128;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int self = blockIdx.x * kWarps + warp;
     WarpSmem<D>& ws = sm.w[warp];
@@ -530,7 +533,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                 const int u = 2 * nb + j, r = min(8 * nb + 2 * c2 + j, nrows - 1);
                 const int pos = e.len - e.qn + r / a.group;
                 sl[u] = a.scale_log2 / __shfl_sync(0xffffffffu, unit_q, 4 * (2 * c2 + j));
-                lim[u] = a.causal ? min(pos, e.len - 1) : e.len - 1;
+                lim[u] = kLean ? pos : a.causal ? min(pos, e.len - 1) : e.len - 1;
                 low[u] = below_window(a, pos);
                 m[u] = kNoKey;
                 up[u] = 0.f;
@@ -598,7 +601,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
                         float l = s[nb][b][k] * (sl[u] * ks);
                         if (masked) {
                             const int key = key0 + 16 * b + r0 + 8 * (k >> 1);
-                            if (key > lim[u] || key <= low[u] || ks == -INFINITY) l = -INFINITY;
+                            const bool hidden = kLean ? key >= e.len || (a.causal && key > lim[u]) ||
+                                                            key <= below_window(a, lim[u])
+                                                      : key > lim[u] || key <= low[u];
+                            if (hidden || ks == -INFINITY) l = -INFINITY;
                         }
                         s[nb][b][k] = l;
                         top[u] = fmaxf(top[u], l);
@@ -640,20 +646,24 @@ __global__ __launch_bounds__(kThreads, 1) void k_attn_rows(const Attn a, const _
             uint32_t pf[NB][2][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                const float lift[2] = {pow2(up[2 * nb]), pow2(up[2 * nb + 1])};
+                const float2 lift = make_float2(pow2(up[2 * nb]), pow2(up[2 * nb + 1]));
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    // (a hidden page's scale may be anything: it meets zeros)
-                    const float w[2] = {fminf(vs[b] * lift[0], kLargestFloat), fminf(vs[b] * lift[1], kLargestFloat)};
-                    float pr[4];
+                    float2 pr[2], l2 = make_float2(L[2 * nb], L[2 * nb + 1]);
+                    const float2 mm = make_float2(-m[2 * nb], -m[2 * nb + 1]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        pr[k] = ex2(s[nb][b][k] - m[2 * nb + (k & 1)]);
-                        L[2 * nb + (k & 1)] += pr[k];
+                    for (int k = 0; k < 2; ++k) {
+                        pr[k] = __fadd2_rn(make_float2(s[nb][b][2 * k], s[nb][b][2 * k + 1]), mm);
+                        pr[k].x = ex2(pr[k].x);
+                        pr[k].y = ex2(pr[k].y);
+                        l2 = __fadd2_rn(l2, pr[k]);
+                        // (the scale last: a hidden page's may be anything, and meets zeros)
+                        pr[k] = __fmul2_rn(__fmul2_rn(pr[k], lift), make_float2(vs[b], vs[b]));
+                        // keys x columns, transposed into the B operand
+                        pf[nb][b][k] = movm(pack_half2(pr[k].x, pr[k].y));
                     }
-                    // keys x columns, transposed into the B operand
-                    pf[nb][b][0] = movm(pack_half2(pr[0] * w[0], pr[1] * w[1]));
-                    pf[nb][b][1] = movm(pack_half2(pr[2] * w[0], pr[3] * w[1]));
+                    L[2 * nb] = l2.x;
+                    L[2 * nb + 1] = l2.y;
                 }
             }
             // e4m3 rows behind the slot's end may hold NaN codes, and 0 NaN is NaN

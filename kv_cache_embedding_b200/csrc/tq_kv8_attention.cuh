@@ -133,7 +133,7 @@ constexpr float kGrow = 8.f, kRoom = 14.f, kNoKey = -1e38f;
 // by up to one), the new up; start: where the largest product is put.  (A row whose
 // values are far below its probabilities: as far as fp32 goes.)
 __device__ __forceinline__ float new_up(float follow, float top, float start) {
-    return fminf(top + follow > kRoom ? start - ceilf(top) : follow, 120.f);
+    return fminf(top + follow > kRoom ? start - ceilf(top) : follow, 100.f);
 }
 
 // The power of two that brings a row's largest magnitude into [2^15, 2^16), the top
