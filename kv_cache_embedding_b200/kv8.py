@@ -35,6 +35,23 @@ _SCALINGS = {"none": B.TQ_ROPE_PLAIN, "linear": B.TQ_ROPE_LINEAR, "ntk": B.TQ_RO
              "parts": B.TQ_ROPE_PARTS}
 
 
+_words = {}  # device: words that no cache has had yet
+
+
+def _status_word(device):
+    """A zero on the device that every stream can use at once: a kernel that writes it
+    would be waited for on one stream alone.  Copies from pageable memory are complete
+    when they return; one in 256 caches pays for it."""
+    if device.type != "cuda" or torch.cuda.is_current_stream_capturing():
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    words = _words.setdefault(device, [])
+    while True:
+        try:
+            return words.pop()
+        except IndexError:
+            words.extend(torch.zeros(256, dtype=torch.int32).to(device).split(1))
+
+
 class _RopeFn(torch.autograd.Function):
     """A linear map: its gradient is the transposed one, again with a gradient."""
 
@@ -113,7 +130,7 @@ class KV8Cache:
         self.table, self.lens, self.refs = table, lens, refs
         self.layers, self.pages, self.heads, self.page, self.d = layers, pages, heads, page, d
         self.slots, self.device = lens.shape[0], k.device
-        self._status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._status = _status_word(k.device)
         self.c = B.tq_kv8_t(d, heads, page, _FORMATS[k.dtype], layers, self.slots, table.shape[1],
                             pages, k.data_ptr(), v.data_ptr(), kscale.data_ptr(),
                             vscale.data_ptr(), table.data_ptr(), lens.data_ptr(), refs.data_ptr(),

@@ -180,3 +180,42 @@ def test_the_library_without_a_status_word(tq_lib, cuda):
                     x.data_ptr(), B.TQ_F32, 256, 128, None, stream)
     k, _ = c.read(0, ints([0], cuda), cu_of([20], cuda), 20, 20, dtype=torch.float32)
     assert ((k - x).abs() <= x.abs().max() / 254 * 1.01).all()
+
+
+def test_a_cache_made_behind_other_work(tq_lib, cuda):
+    """A cache over an engine's tensors can be used on any stream at once: its status
+    word does not wait for the stream on which it was made."""
+    parts = make_cache(tq_lib, cuda, page=16, slots=2, max_pages=4, pages=2)
+    slots, one = ints([0], cuda), ints([1], cuda)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # what the word's memory may hold
+        torch.full((512,), 0xF8, dtype=torch.uint8, device=cuda)
+        torch.full((4,), -1, dtype=torch.int32, device=cuda)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        c = tq_lib.KV8Cache(parts.k, parts.v, parts.kscale, parts.vscale, parts.table, parts.lens, parts.refs)
+    c.reserve(slots, one)
+    c.status()
+    assert int(c.lens[0]) == 1
+
+
+def test_many_caches(tq_lib, cuda):
+    """Each with a status of its own, however many there are, also one made in a
+    capture."""
+    caches = [make_cache(tq_lib, cuda, page=16, slots=1, max_pages=1, pages=1, d=64) for _ in range(300)]
+    assert len({c._status.data_ptr() for c in caches}) == 300
+    caches[7].reserve(ints([0], cuda), ints([17], cuda))
+    for i, c in enumerate(caches):
+        if i == 7:
+            refused(tq_lib, c, "ARG")
+        else:
+            c.status()
+    parts, slots, one = caches[0], ints([0], cuda), ints([1], cuda)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c = tq_lib.KV8Cache(parts.k, parts.v, parts.kscale, parts.vscale, parts.table, parts.lens, parts.refs)
+        c.reserve(slots, one)
+    g.replay()
+    c.status()
+    assert parts.lens.tolist() == [1]
