@@ -10,10 +10,10 @@
 // block reduction and nothing is written twice: new rows are loaded once into
 // registers, turned, reduced, rounded and stored; the page's old rows are touched
 // only when the scale grows.  Bound by issue slots and by its loads' latency at half
-// of the warps for prompts (28105 tokens x 8 heads of 128, bf16 to e4m3: 53 us, 3.3
-// TB/s, 64 us with half of each key turned; 512 threads of one item beat 256 of two,
+// of the warps for prompts (28105 tokens x 8 heads of 128, bf16 to e4m3: 55 us, 3.2
+// TB/s, 66 us with half of each key turned; 512 threads of one item beat 256 of two,
 // 53 against 65, and 4 heads a block one head, 53 against 78), by the chain length ->
-// table -> scale for single tokens (4 us for 64).
+// table -> scale for single tokens (4.6 us for 64).
 #include "tq_kv8.cuh"
 #include "tq_rope.cuh"
 
@@ -229,18 +229,18 @@ __global__ __launch_bounds__(VEC == 8 ? 1024 : 256) void k_append(
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < blockDim.x / 32 ? red[lane] : 0u));
         if (held) return;  // (before the first store)
         float s = fmaxf(s_old, __fdiv_rn(top, code_max<FMT>()));
-        float up = 1.f;
+        float up = 1.f, inv = s > 0.f ? __frcp_rn(s) : 0.f;
         if (s < 1.17549435e-38f) {  // below fp32's normal range:
             // a few units of 2^-149 are rounded up, so that no code leaves its range;
             if (fmaf(s, code_max<FMT>(), -top) < 0.f) s = __uint_as_float(__float_as_uint(s) + 1);
             up = 18446744073709551616.f;  // a reciprocal may overflow: all times 2^64
+            inv = s > 0.f ? __frcp_rn(s * up) : 0.f;
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
                 for (int e = 0; e < 2 * VEC; ++e) val[i][e] *= up;
         }
         if (threadIdx.x == 0) a.scale[kv][ph] = s;
-        const float inv = s > 0.f ? __frcp_rn(s * up) : 0.f;
         uint8_t* codes = a.codes[kv] + (ph << v.page_log2) * v.d;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -338,7 +338,8 @@ constexpr int kReadItems = 4;  // of 16 codes, a thread
 // (and, of an entry with more tokens than the launch was sized for, every bps-th such
 // run behind it).  The lookups of a thread's items, then their codes, are on their way
 // together.  Rows that no entry owns become 0.
-// Bound by HBM: 28306 tokens x 8 heads of 128, e4m3 to bf16, 38 us, 4.6 TB/s.
+// 28306 tokens x 8 heads of 128, e4m3 to bf16: 38 us, 4.6 TB/s, 70 % of the copy rate;
+// the divisions that find an item's token, head and chunk are the rest.
 template <typename T, int FMT>
 __global__ __launch_bounds__(kReadThreads) void k_read(View v, const int32_t* slots, const int32_t* begin,
                                                        const int32_t* cu, int ns, int bps, int tokens, int64_t total,

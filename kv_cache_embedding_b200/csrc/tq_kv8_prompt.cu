@@ -31,12 +31,13 @@
 // Every wait is bounded (1 s); a warp that gives up sets the abort flag and the
 // call's status.
 //
-// Measured (4096 tokens x 32 heads of 128 over 16384 keys, causal): 1030 us, 934
-// TFLOP/s.  The softmax bounds it: 64 keys take a stage 2100 cycles against 600
-// of MMAs, by issue slots (some 5 instructions an element of S, shared with the
-// conversion's) and the latency of its chain.  Tried and slower: a quarter or half
-// of the exponentials as polynomials on the FMA pipe (1087, 1181 us), whole tiles
-// (1101 us), one warp for both stages' MMAs (1189 us).
+// Measured (4096 tokens x 32 heads of 128 over 16384 keys, causal): 1058 us, 909
+// TFLOP/s.  Latency bounds it: two stages' half tiles are some 1000 cycles of
+// exponentials and 1000 of MMAs and take 2100, with half of the issue slots and 43 % of
+// the tensor pipe in use; one softmax warp a scheduler and stage runs a chain S ->
+// maximum -> exponentials -> P.  Tried and slower: a quarter or half of the exponentials
+// as polynomials on the FMA pipe (1087 and 1181 us against 1040), whole tiles (1101),
+// one warp for both stages' MMAs (1189).
 #include "tq_kv8_attention.cuh"
 #include "tq_score_common.cuh"
 
