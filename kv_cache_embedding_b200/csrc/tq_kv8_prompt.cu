@@ -340,16 +340,12 @@ __global__ __launch_bounds__(kPThreads, 1) void k_attn_prompt(const Attn a,
                     tg[g] = -INFINITY;
                 }
                 const uint32_t absent = sm.absent[rg] >> 4 * h & 15u;
-                // a half tile that a mask touches, or with rows of logits beyond 2^22 (an
-                // item's first: that could be; rows that are not finite aside): there logits
-                // are rounded before m is taken off.  What the fused product of the other
-                // way keeps of such would be whole units
-                const float size_m = fabsf(m);
-                bool far = size_m > 4194304.f && size_m < -kNoKey;
-                if (halves == first) {
-                    const float most = fmaxf(max3(cg[0], cg[1], cg[2]), cg[3]);
-                    far = most > 4194304.f / (65536.f * code_max<FMT>() * D) && most < 1e25f;
-                }
+                // a half tile that a mask touches, or with rows whose logits may pass 2^22
+                // (rows that are not finite aside): there logits are rounded before m is taken
+                // off.  What the fused product of the other way keeps of such would be whole
+                // units
+                const float most = fmaxf(max3(cg[0], cg[1], cg[2]), cg[3]);
+                const bool far = most > 4194304.f / (65536.f * code_max<FMT>() * D) && most < 1e25f;
                 const bool masked = __any_sync(0xffffffffu, key0 + kPH - 1 > lim || key0 <= low || absent || far);
                 // 32 keys are on their way while the 32 before them are looked at
                 if (masked) {

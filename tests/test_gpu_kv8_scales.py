@@ -174,3 +174,21 @@ def test_large_logits(tq_lib, cuda, count, page, top):
     far = (out.cpu().double() - want).abs()
     assert (far <= want.abs() * (2.0 ** -11 + U[torch.bfloat16]) * (1 + 2.0 ** -8) + 1e-12).all()
     assert ((lse.cpu().double() / abs(top) - 1).abs() <= 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("count", [1, 3, 40])
+@pytest.mark.parametrize("at", [0, 70, 200, 299])
+@pytest.mark.parametrize("top", [3e7, 1e9, 1e12])
+def test_a_large_logit_among_small_ones(tq_lib, cuda, count, at, top):
+    """One key's logit, wherever it lies, is the only large one."""
+    n = 300 + count
+    c = fill(tq_lib, cuda, "i8", 1, 128, 64, [n], scale_range=(0.9, 1.1))
+    c.k.zero_()
+    c.kscale.fill_(0.01)
+    c.k[0, int(c.table[0, at // 64]), 0, at % 64] = 100
+    q = torch.ones(count, 2, 128, dtype=torch.bfloat16, device=cuda)
+    out = c.attention(0, q, cu_of([count], cuda), count, scale=top / 128)
+    c.status()
+    want = values(c, "v", 0, 0, n)[0, at]
+    far = (out.cpu().double() - want).abs()
+    assert (far <= want.abs() * (2.0 ** -11 + U[torch.bfloat16]) * (1 + 2.0 ** -8) + 1e-12).all()
