@@ -519,15 +519,16 @@ TQ_API int tq_kv8_read(const tq_kv8_t *c, int layer, int ns, const int32_t *d_sl
  * in rows that do not see it.)
  * d_q, d_out: [total_q][heads_q][d] of q_dtype (TQ_BF16 or TQ_F16); q with
  * strides in elements (multiples of 8, the base 16-byte aligned), out
- * contiguous.  d_lse: [total_q][heads_q] fp32 or NULL.  heads_q a multiple of
- * heads, at most 128 times as many, total_q times that multiple below 2^31 - 2^16
- * (else TQ_ERR_UNSUPPORTED).
+ * contiguous; rows behind cu[ns] stay as they were.  d_lse: [total_q][heads_q] fp32
+ * or NULL.  heads_q a multiple of heads, at most 128 times as many, total_q times that
+ * multiple below 2^31 - 2^16 (else TQ_ERR_UNSUPPORTED).
  * d_ws: >= tq_kv8_workspace_bytes(TQ_KV8_OP_ATTENTION, c, ns, total_q, max_q,
  * heads_q), any contents; calls that overlap on the GPU need workspaces of their
  * own.  A cu beyond total_q, or an entry of more than max_q tokens where max_q tokens
  * have 16 rows at most (tokens x group), refuses the call: TQ_ERR_ARG in d_ws and
- * c->d_status, every row as one that sees no key.  The result does not depend on what else runs, nor on earlier calls.  A
- * captured call that has timed out is to be captured anew. */
+ * c->d_status, every row as one that sees no key.  The result does not depend on what
+ * else runs, nor on earlier calls.  A captured call that has timed out is to be
+ * captured anew. */
 TQ_API int tq_kv8_attention(const tq_kv8_t *c, int layer, int ns, const int32_t *d_slots,
                             const int32_t *d_cu, int64_t total_q, int max_q, int heads_q,
                             const void *d_q, int q_dtype, int64_t q_ts, int64_t q_hs, float scale,

@@ -24,9 +24,9 @@
 // (K: plain ldmatrix, coordinates permuted alike on both sides; V: transposing
 // ldmatrix of byte pairs, the halves sorted out by byte permutes).
 //
-// Measured: 4 x 131072 keys x 8 heads of 128, one token of 32 heads: 190 us, 5.6 TB/s
+// Measured: 4 x 131072 keys x 8 heads of 128, one token of 32 heads: 191 us, 5.6 TB/s
 // (a copy runs at 6.55); 64 ragged sequences 104 us, 5.2 TB/s; one sequence of 500
-// keys 9.4 us, a chain of lookups, two tiles of dependent instructions and the join.
+// keys 9.5 us, a chain of lookups, two tiles of dependent instructions and the join.
 // With 8 warps of 16 rows and lookups in line: 233, 122 and 10.4 us.  16 rows are bound
 // by issue and by what is spilled of 168 registers: 184 us for keys that one token reads
 // in 95 (16 x 16384).

@@ -31,7 +31,7 @@
 // Every wait is bounded (1 s); a warp that gives up sets the abort flag and the
 // call's status.
 //
-// Measured (4096 tokens x 32 heads of 128 over 16384 keys, causal): 1058 us, 909
+// Measured (4096 tokens x 32 heads of 128 over 16384 keys, causal): 1055 us, 911
 // TFLOP/s.  Latency bounds it: two stages' half tiles are some 1000 cycles of
 // exponentials and 1000 of MMAs and take 2100, with half of the issue slots and 43 % of
 // the tensor pipe in use; one softmax warp a scheduler and stage runs a chain S ->
